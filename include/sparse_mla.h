@@ -418,6 +418,230 @@ smla_status sparse_mla_indexer(const smla_indexer_shape* shape, const void* q, c
                                const int32_t* page_table, const int32_t* ctx_len, float* scores,
                                int32_t* indices, void* stream);
 
+/* ------------------------------------------------------- rotary positions
+ * The rotation by position of the query's (and the keys') rotary part, which
+ * the decode expects done: of each head's `dim` dims, rope_dim dims from
+ * `offset` on are turned in pairs (a, b), pair i of the token at position p:
+ *   y_a = m (a cos(p f_i) - b sin(p f_i)),   y_b = m (a sin(p f_i) + b cos(p f_i))
+ * and the others passed on.  Frequencies f_i = base^(-2 i / rope_dim)
+ * radians per position, scaled for contexts longer than the model's own:
+ *   linear  f_i / factor
+ *   YaRN    f_i (1 - r_i) + f_i / factor * r_i, r_i = (i - lo) / (hi - lo) held
+ *           to [0, 1], lo = floor(P(beta_fast)), hi = ceil(P(beta_slow)) held
+ *           to [0, rope_dim - 1] (hi - lo at least 0.001), P(t) = rope_dim
+ *           ln(original_ctx / (2 pi t)) / (2 ln base): pairs that turn more
+ *           than beta_fast times over the original context keep their
+ *           frequency, pairs that turn less than beta_slow times are stretched
+ * m = mscale multiplies cos and sin (1, or YaRN's attention factor).
+ * The source pages split the head into 448 or 512 dims and 64 rope dims
+ * ([Design] "Kernel Structure Analysis") and leave the rotation to the model. */
+#define SMLA_ROPE_MAX_DIM 256
+
+typedef enum { SMLA_ROPE_INTERLEAVED = 0 /* pairs (2 i, 2 i + 1) */,
+               SMLA_ROPE_HALF = 1 /* pairs (i, i + rope_dim / 2) */ } smla_rope_layout;
+typedef enum { SMLA_ROPE_SCALING_NONE = 0, SMLA_ROPE_SCALING_LINEAR = 1, SMLA_ROPE_SCALING_YARN = 2 } smla_rope_scaling;
+typedef enum { SMLA_DTYPE_BF16 = 0, SMLA_DTYPE_FP16 = 1, SMLA_DTYPE_FP32 = 2 } smla_dtype;
+
+typedef struct {
+  int32_t rope_dim;       /* even, 2 .. 256                                     */
+  int32_t layout;         /* smla_rope_layout                                   */
+  int32_t scaling;        /* smla_rope_scaling                                  */
+  int32_t original_ctx;   /* YaRN: context length before the extension          */
+  double base;            /* > 0 (YaRN: > 1), e.g. 10000                        */
+  double factor;          /* linear, YaRN: > 0                                  */
+  double beta_fast;       /* YaRN, e.g. 32                                      */
+  double beta_slow;       /* YaRN, e.g. 1                                       */
+  double mscale;          /* e.g. 1                                             */
+} smla_rope_config;
+
+/* What the rotation works from: each frequency as a 64-bit fraction of a
+ * turn, so that the angle of any int32 position is exact to 2^-32 turns.
+ * Plain host data, filled once by sparse_mla_rope_init and passed by pointer
+ * to the calls (which copy it). */
+typedef struct {
+  int32_t rope_dim;
+  int32_t layout;
+  float mscale;
+  int32_t reserved;
+  uint64_t step[SMLA_ROPE_MAX_DIM / 2];   /* f_i / (2 pi) * 2^64 modulo 2^64     */
+} smla_rope_table;
+
+/* Fills *table; a host computation, no CUDA call. */
+smla_status sparse_mla_rope_init(const smla_rope_config* config, smla_rope_table* table);
+
+typedef struct {
+  int64_t tokens;          /* 0 and up (0: nothing is launched)                  */
+  int32_t heads;           /* 1 .. 65536                                         */
+  int32_t dim;             /* dims per head that y receives, 2 .. 65536          */
+  int32_t offset;          /* first rotated dim, 0 .. dim - rope_dim             */
+  int32_t dtype;           /* smla_dtype of x and y                              */
+  int32_t transpose;       /* 1: the gradient of the rotation (angles negated)   */
+  int32_t reserved;        /* must be 0                                          */
+  int64_t x_token_stride;  /* strides in elements; the dims of a head are        */
+  int64_t x_head_stride;   /* contiguous.  x's may be 0 (one row for all heads)  */
+  int64_t y_token_stride;
+  int64_t y_head_stride;
+} smla_rope_shape;
+
+/* y[t, h, :] = x[t, h, :] with its rotary part turned by positions[t].
+ *   x, y       device memory of `dtype`, aligned to the element; 16-byte
+ *              aligned rows and edges take the fast path
+ *   positions  [tokens] int32, any value
+ * y may be x (same strides: the rotated dims alone are read and written);
+ * otherwise their memory must not overlap.  Computed in fp32, rounded once.
+ * With transpose the call is the gradient of the rotation with respect to x
+ * (x is then the gradient of y), which undoes the rotation when mscale = 1:
+ * DeepSeek-V4 rows carry rotated dims in the value too, and its output's
+ * last 64 dims are turned back this way.  Rows of y may not share memory
+ * (SMLA_ERR_INVALID_ARG where the strides say so). */
+smla_status sparse_mla_rope(const smla_rope_shape* shape, const smla_rope_table* table, const void* x,
+                            const int32_t* positions, void* y, void* stream);
+
+/* ----------------------------------------------------------- cache append
+ * Writes new tokens into the cache that the decode reads: normalised,
+ * rotated, encoded in the cache's layout and stored, in one pass over the
+ * tokens ([Design] "The Agent Reasoning", "Cache Layout Understanding", has
+ * the layouts; how rows get there is left to the serving engine).  Token i's
+ * row x_i of 576 dims (512 for SMLA_KV_DSV4_PAGED) becomes
+ *   dims 0 .. 511   norm_weight * x / sqrt(mean(x[0:512]^2) + eps), or x
+ *                   where norm_weight is NULL
+ *   the last 64     turned by positions[i] (after the norm, where that covers
+ *                   them), or as they are where the table is NULL
+ * and is stored as
+ *   SMLA_KV_BF16                bf16
+ *   SMLA_KV_FP8_E4M3_ROWSCALE   scale = amax / 448 over the row (1 for a row of
+ *                               zeros, at least 2^-126), codes e4m3(x / scale)
+ *   SMLA_KV_DSV4_PAGED          per 64 of the first 448 dims the smallest power
+ *                               of two with amax <= 448 * scale (at least
+ *                               2^-126), codes e4m3(x / scale); the last 64
+ *                               dims bf16; the scale block's eighth byte 0
+ * computed in fp32, each stored value rounded once (to nearest, ties to
+ * even). */
+typedef struct {
+  int64_t tokens;          /* 0 .. 2^31 - 1 (0: nothing is launched)             */
+  int64_t x_stride;        /* elements from token to token: >= the row, or 0     */
+  int64_t num_kv_rows;     /* physical rows in the pool                          */
+  int32_t x_dtype;         /* smla_dtype                                         */
+  int32_t kv_dtype;        /* smla_kv_dtype                                      */
+  int32_t page_size;       /* 0: flat pool, slots are physical rows; 64: slots   */
+  int32_t pages_per_seq;   /* are logical positions through page_table           */
+  int32_t batch;           /* sequences in page_table (paged)                    */
+  float eps;               /* >= 0                                               */
+  int32_t reserved;        /* must be 0                                          */
+} smla_append_shape;
+
+/*   x             [tokens, 576] (or 512), rows x_stride elements apart
+ *   norm_weight   [512] fp32, 16-byte aligned, or NULL
+ *   table         host memory, rope_dim 64, or NULL
+ *   positions     [tokens] int32, the rotation's (with a table)
+ *   slots         [tokens] int32: where each row goes.  Negative: the token is
+ *                 skipped.  (After an eviction a token's place in the cache
+ *                 is no longer its position, hence the two arrays.)
+ *   seq           [tokens] int32, each token's sequence, for a paged pool; NULL:
+ *                 the tokens are batch equal runs, sequence by sequence
+ *   page_table    [batch, pages_per_seq] int32 (paged), else NULL
+ *   kv_cache      the pool, written; kv_row_scale [num_kv_rows] fp32 (fp8)
+ * A slot, sequence or page outside its range writes nothing and sets bit 2
+ * of the device error word.  Two tokens of one call may not name the same
+ * row (it would hold parts of both).  Rows that no token names keep their
+ * bytes.  Values are expected finite. */
+smla_status sparse_mla_cache_append(const smla_append_shape* shape, const void* x, const float* norm_weight,
+                                    const smla_rope_table* table, const int32_t* positions, const int32_t* slots,
+                                    const int32_t* seq, const int32_t* page_table, void* kv_cache,
+                                    float* kv_row_scale, void* stream);
+
+/* ------------------------------------------------------ attention weights
+ * How much attention each listed row received in a decode step, summed over
+ * the heads: with s_j = scale <q[b, t, h], k_j> as in sparse_mla_decode,
+ *   weights[b, t, j] = sum_h exp(s_j - lse[b, t, h])        (fp32)
+ * for the entries of the index lists, 0 for entries that are padding (or out
+ * of range, which sets bit 2 of the device error word).  lse is the
+ * decode's; the weights of a list then sum to 64 (one per head).  A head whose
+ * lse is -inf takes no part. */
+
+/* Shapes, layouts and checks as for sparse_mla_decode (shape->nsplit is not
+ * used); lse [B, 64] fp32 ([B, T, 64]) is read, weights [B, topk] fp32
+ * ([B, T, topk]) written. */
+smla_status sparse_mla_attn_weights(const smla_shape* shape, const void* q, const void* kv_cache,
+                                    const float* kv_row_scale, const int32_t* page_table, const int32_t* indices,
+                                    const float* lse, float scale, float* weights, void* stream);
+
+/* Sums weights onto the positions they were given to:
+ *   acc[b, p] = decay * acc[b, p] + sum of weights[b, e] over indices[b, e] = p
+ *   batch     1 .. 65535
+ *   entries   list entries per sequence, topk (times tokens_per_seq),
+ *             1 .. 2^28
+ *   max_ctx   width of acc, 1 .. 2^20
+ *   indices   [batch, entries] int32 logical positions; negative entries take
+ *             no part; one at or past max_ctx takes none and sets bit 2 of
+ *             the device error word.  A position may stand in the list many
+ *             times.
+ *   weights   [batch, entries] fp32
+ *   decay     0 .. 1: what older steps count for (1: plain sums; positions
+ *             that got nothing are then not written)
+ *   acc       [batch, max_ctx] fp32, updated
+ * The sum of a position is taken in 64-bit fixed point whose unit is at most
+ * 2^-62 of (entries, rounded up to a power of two) * twice the sequence's
+ * largest |weight|, so it does not depend on the order of the entries; it is
+ * added in fp64 and rounded once.  A NaN or infinite weight makes its
+ * position NaN. */
+smla_status sparse_mla_accumulate_weights(int32_t batch, int64_t entries, int32_t max_ctx, const int32_t* indices,
+                                          const float* weights, float decay, float* acc, void* stream);
+
+/* --------------------------------------------------------------- eviction
+ * Bounds a sequence's paged cache: of its n = ctx_len[b] positions at most
+ * `budget` are kept -- all of them if n <= budget; otherwise the first `sinks`,
+ * the last `recent`, and of the others those with the largest accumulated
+ * weight (ties to the lower position, as in the indexer's selection; a NaN
+ * counts as the lowest).  The kept positions move, in ascending order, to
+ * positions 0, 1, ...: in the cache, its scales, the indexer's keys and the
+ * accumulated weights.  Rows keep the rotation of their original position. */
+typedef struct {
+  int32_t batch;              /* 1 .. 65535                                       */
+  int32_t max_ctx;            /* width of acc, 1 .. 2^20; every ctx_len is at     */
+                              /* most this (larger ones are clamped, bit 2)      */
+  int32_t budget;             /* 1 .. max_ctx                                     */
+  int32_t sinks, recent;      /* >= 0, sinks + recent <= budget                   */
+  int32_t kv_dtype;           /* smla_kv_dtype; pages of 64 rows                  */
+  int32_t pages_per_seq;      /* width of page_table; 64 * it >= max_ctx          */
+  int32_t new_pages_per_seq;  /* width of new_page_table; 64 * it >= budget       */
+  int64_t num_kv_rows;        /* rows in the pool, a multiple of 64               */
+  int64_t num_key_rows;       /* rows in the indexer's key cache, a multiple of   */
+                              /* 64; 0: no key cache                              */
+} smla_evict_shape;
+
+/* The selection.
+ *   acc      [batch, max_ctx] fp32, ctx_len [batch] int32: read
+ *   kept     [batch, budget] int32, written: the kept positions ascending,
+ *            then -1
+ *   new_len  [batch] int32, written: min(n, budget).  May be ctx_len.
+ *   acc_out  [batch, max_ctx] fp32, written: the kept positions' weights, then
+ *            zeros up to n; entries from n on keep their values.  May be
+ *            acc. */
+smla_status sparse_mla_evict_select(const smla_evict_shape* shape, const float* acc, const int32_t* ctx_len,
+                                    int32_t* kept, int32_t* new_len, float* acc_out, void* stream);
+
+/* The compaction, with kept and new_len as sparse_mla_evict_select writes them:
+ * row kept[b, i] of the sequence moves to row i, i < new_len[b].
+ *   page_table      [batch, pages_per_seq] int32
+ *   new_page_table  NULL: in place -- no page may then belong to two sequences
+ *                   of the batch.  Else [batch, new_pages_per_seq] int32: pages
+ *                   that page_table does not name, so the old rows stay as
+ *                   they are (a prefix that other sequences share is left
+ *                   alone).
+ *   kv_cache, kv_row_scale (fp8), k_cache ([num_key_rows, 128] bf16, or NULL)
+ * Rows of the destination from new_len[b] on keep their bytes.  A page outside
+ * the pool moves nothing and sets bit 2 of the device error word. */
+smla_status sparse_mla_evict_compact(const smla_evict_shape* shape, const int32_t* kept, const int32_t* new_len,
+                                     const int32_t* page_table, const int32_t* new_page_table, void* kv_cache,
+                                     float* kv_row_scale, void* k_cache, void* stream);
+
+/* Both: two launches on `stream`. */
+smla_status sparse_mla_evict(const smla_evict_shape* shape, const float* acc, const int32_t* ctx_len, int32_t* kept,
+                             int32_t* new_len, float* acc_out, const int32_t* page_table,
+                             const int32_t* new_page_table, void* kv_cache, float* kv_row_scale, void* k_cache,
+                             void* stream);
+
 #ifdef __cplusplus
 }
 #endif

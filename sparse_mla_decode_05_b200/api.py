@@ -47,6 +47,40 @@ class IndexerShape(ctypes.Structure):
 
 
 IX_HEADS, IX_DIM = 64, 128
+ROPE_MAX_DIM = 256
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}          # smla_dtype
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("rope_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("original_ctx", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("mscale", ctypes.c_double)]
+
+
+class RopeTableData(ctypes.Structure):
+    _fields_ = [("rope_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("step", ctypes.c_uint64 * (ROPE_MAX_DIM // 2))]
+
+
+class RopeShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("offset", ctypes.c_int32), ("dtype", ctypes.c_int32), ("transpose", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
+
+
+class AppendShape(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("num_kv_rows", ctypes.c_int64),
+                ("x_dtype", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("batch", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class EvictShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("max_ctx", ctypes.c_int32), ("budget", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("pages_per_seq", ctypes.c_int32), ("new_pages_per_seq", ctypes.c_int32),
+                ("num_kv_rows", ctypes.c_int64), ("num_key_rows", ctypes.c_int64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -89,6 +123,24 @@ def _load() -> ctypes.CDLL:
     lib.sparse_mla_host_staging_size.argtypes = [SP]
     lib.sparse_mla_decode_host.restype = I32
     lib.sparse_mla_decode_host.argtypes = [SP, P, P, P, P, P, F32, P, P, P, SZ, P]
+    lib.sparse_mla_rope_init.restype = I32
+    lib.sparse_mla_rope_init.argtypes = [ctypes.POINTER(RopeConfig), ctypes.POINTER(RopeTableData)]
+    TP = ctypes.POINTER(RopeTableData)
+    lib.sparse_mla_rope.restype = I32
+    lib.sparse_mla_rope.argtypes = [ctypes.POINTER(RopeShape), TP, P, P, P, P]
+    lib.sparse_mla_cache_append.restype = I32
+    lib.sparse_mla_cache_append.argtypes = [ctypes.POINTER(AppendShape), P, P, TP, P, P, P, P, P, P, P]
+    lib.sparse_mla_attn_weights.restype = I32
+    lib.sparse_mla_attn_weights.argtypes = [SP, P, P, P, P, P, P, F32, P, P]
+    lib.sparse_mla_accumulate_weights.restype = I32
+    lib.sparse_mla_accumulate_weights.argtypes = [I32, ctypes.c_int64, I32, P, P, F32, P, P]
+    EP = ctypes.POINTER(EvictShape)
+    lib.sparse_mla_evict_select.restype = I32
+    lib.sparse_mla_evict_select.argtypes = [EP, P, P, P, P, P, P]
+    lib.sparse_mla_evict_compact.restype = I32
+    lib.sparse_mla_evict_compact.argtypes = [EP, P, P, P, P, P, P, P, P]
+    lib.sparse_mla_evict.restype = I32
+    lib.sparse_mla_evict.argtypes = [EP, P, P, P, P, P, P, P, P, P, P, P]
     return lib
 
 
@@ -527,3 +579,332 @@ def indexer(q, w, k_cache, page_table, ctx_len, topk: int, *, max_ctx: int | Non
     plan = IndexerPlan(q, w, k_cache, page_table, ctx_len, topk, max_ctx=max_ctx)
     plan.run()
     return plan.indices, plan.scores
+
+
+# ------------------------------------------- around the decode: common parts
+def _check_device(dev, **tensors):
+    """Every given tensor lies on the CUDA device ``dev``."""
+    for name, t in tensors.items():
+        if t is not None and (not t.is_cuda or t.device != dev):
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+
+
+def _check_tensor(name, t, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+class _Plan:
+    """A call with its arguments marshalled once.  run() is one call into the
+    library, on the current stream of the tensors' device unless a stream is
+    given.  The tensors must stay alive and keep their addresses while the
+    plan is in use; the plan holds references to them."""
+
+    _call = None        # name of the entry point
+    _empty = False      # nothing to do (no tokens)
+
+    def _ready(self, dev, args, keep):
+        self._device, self._args, self._keep = dev, args, keep
+        self._fn = getattr(lib, self._call)
+
+    def run(self, stream=None):
+        if self._empty:
+            return
+        dev = self._device
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        s = s.cuda_stream if hasattr(s, "cuda_stream") else s
+        if torch.cuda.current_device() == dev.index:
+            st = self._fn(*self._args, s)
+        else:
+            with torch.cuda.device(dev):
+                st = self._fn(*self._args, s)
+        if st != 0:
+            raise SmlaError(st, self._call)
+
+
+def _cache_kind(kv):
+    """smla_kv_dtype of a cache tensor, as decode() reads it."""
+    if is_dsv4(kv):
+        return KV_DSV4_PAGED
+    if kv.dim() != 2 or kv.shape[1] != D_QK or kv.dtype not in (torch.bfloat16, torch.uint8):
+        raise ValueError("kv must be [N, 576] bf16 or uint8 (fp8 e4m3fn codes), or uint8 [pages, 37376] "
+                         "DeepSeek-V4 pages")
+    return KV_FP8_E4M3_ROWSCALE if kv.dtype == torch.uint8 else KV_BF16
+
+
+def _check_cache(kv, kv_row_scale):
+    kind = _cache_kind(kv)
+    if not kv.is_contiguous():
+        raise ValueError("kv must be contiguous")
+    if (kind == KV_FP8_E4M3_ROWSCALE) != (kv_row_scale is not None):
+        raise ValueError("an fp8 cache needs kv_row_scale, the other caches none")
+    if kv_row_scale is not None:
+        _check_tensor("kv_row_scale", kv_row_scale, torch.float32, (kv.shape[0],))
+    return kind
+
+
+# ------------------------------------------------------------------ rotary
+class RopeTable:
+    """Frequencies of a rotary embedding over ``rope_dim`` dims, for rope()
+    and cache_append().  ``interleaved``: pairs (2 i, 2 i + 1), else (i, i +
+    rope_dim / 2).  ``scaling``: None, "linear" (positions divided by
+    ``factor``) or "yarn" (``factor``, ``original_ctx``, ``beta_fast``,
+    ``beta_slow``).  ``mscale`` multiplies cos and sin.  Host data only."""
+
+    def __init__(self, rope_dim: int = 64, *, base: float = 10000.0, interleaved: bool = True,
+                 scaling: str | None = None, factor: float = 1.0, original_ctx: int = 0, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, mscale: float = 1.0):
+        kinds = {None: 0, "linear": 1, "yarn": 2}
+        if scaling not in kinds:
+            raise ValueError('scaling must be None, "linear" or "yarn"')
+        cfg = RopeConfig(rope_dim, 0 if interleaved else 1, kinds[scaling], original_ctx, base, factor, beta_fast,
+                         beta_slow, mscale)
+        self.data = RopeTableData()
+        st = lib.sparse_mla_rope_init(ctypes.byref(cfg), ctypes.byref(self.data))
+        if st != 0:
+            raise SmlaError(st, "sparse_mla_rope_init")
+        self.rope_dim, self.interleaved, self.mscale = rope_dim, interleaved, mscale
+
+    def turns(self):
+        """Fraction of a turn per position of each pair (float64)."""
+        return [self.data.step[i] / 2.0 ** 64 for i in range(self.rope_dim // 2)]
+
+
+def _token_stride(name, t):
+    """Stride between tokens of a [..., heads, dim] tensor whose leading dims
+    walk memory evenly."""
+    lead, strides = t.shape[:-2], t.stride()[:-2]
+    if not lead:
+        return 0
+    stride, size = None, 1
+    for n, st in zip(reversed(lead), reversed(strides)):
+        if n == 1:
+            continue
+        if stride is None:
+            stride, size = st, n
+        elif st != stride * size:
+            raise ValueError(f"{name}: the token dims must be evenly strided")
+        else:
+            size *= n
+    return 0 if stride is None else stride
+
+
+class RopePlan(_Plan):
+    """rope() with its arguments marshalled once; the result is ``out``."""
+
+    _call = "sparse_mla_rope"
+
+    def __init__(self, x, positions, table: RopeTable, *, offset: int | None = None, transpose: bool = False, out=None):
+        if x.dim() < 2 or x.dtype not in DTYPES:
+            raise ValueError("x must be [..., heads, dim] bf16, fp16 or fp32")
+        heads, dim = x.shape[-2:]
+        lead = tuple(x.shape[:-2])
+        if offset is None:
+            offset = dim - table.rope_dim
+        if offset < 0 or offset + table.rope_dim > dim:
+            raise ValueError("the rotated dims must lie inside the head")
+        if positions.dtype != torch.int32 or tuple(positions.shape) != lead or not positions.is_contiguous():
+            raise ValueError("positions must be contiguous int32 of x's leading shape")
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if out.dtype != x.dtype or out.shape != x.shape:
+            raise ValueError("out must have x's shape and dtype")
+        _check_device(x.device, x=x, positions=positions, out=out)
+        for name, t in (("x", x), ("out", out)):
+            if dim > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{name}: the dims of a head must be contiguous")
+        self.out = out
+        self._empty = x.numel() == 0
+        self.shape = RopeShape(positions.numel(), heads, dim, offset, DTYPES[x.dtype], int(transpose), 0,
+                               _token_stride("x", x), x.stride(-2), _token_stride("out", out), out.stride(-2))
+        self._ready(x.device, (ctypes.byref(self.shape), ctypes.byref(table.data), _ptr(x), _ptr(positions), _ptr(out)),
+                    (x, positions, table, out))
+
+
+def rope(x, positions, table: RopeTable, *, offset: int | None = None, transpose: bool = False, out=None):
+    """x [..., heads, dim] with dims [offset, offset + rope_dim) of every head
+    (default: the last ones) turned by the token's position; positions
+    [...] int32.  ``out`` may be x (in place), or a view such as the rotary
+    part of a larger query.  ``transpose``: the gradient of the rotation with
+    respect to x, given the gradient of its result (for mscale 1 also its
+    inverse)."""
+    plan = RopePlan(x, positions, table, offset=offset, transpose=transpose, out=out)
+    plan.run()
+    return plan.out
+
+
+# ------------------------------------------------------------------ append
+class CacheAppendPlan(_Plan):
+    """cache_append() with its arguments marshalled once."""
+
+    _call = "sparse_mla_cache_append"
+
+    def __init__(self, x, kv, slots, *, kv_row_scale=None, page_table=None, page_size: int = 0, seq=None,
+                 norm_weight=None, eps: float = 1e-6, rope: RopeTable | None = None, positions=None):
+        kind = _check_cache(kv, kv_row_scale)
+        width = D_V if kind == KV_DSV4_PAGED else D_QK
+        if x.dim() != 2 or x.shape[1] != width or x.dtype not in DTYPES or x.stride(1) != 1:
+            raise ValueError(f"x must be [tokens, {width}] bf16, fp16 or fp32 with contiguous rows")
+        n = x.shape[0]
+        _check_tensor("slots", slots, torch.int32, (n,))
+        if (page_size != 0) != (page_table is not None):
+            raise ValueError("page_size and page_table go together")
+        if kind == KV_DSV4_PAGED and page_size != 64:
+            raise ValueError("DeepSeek-V4 pages are paged: page_size must be 64")
+        if page_table is not None and (page_table.dtype != torch.int32 or page_table.dim() != 2
+                                       or not page_table.is_contiguous()):
+            raise ValueError("page_table must be contiguous int32 [B, pages_per_seq]")
+        if seq is not None:
+            if page_table is None:
+                raise ValueError("seq goes with a page_table")
+            _check_tensor("seq", seq, torch.int32, (n,))
+        if norm_weight is not None:
+            _check_tensor("norm_weight", norm_weight, torch.float32, (D_V,))
+        if (rope is None) != (positions is None):
+            raise ValueError("rope and positions go together")
+        if positions is not None:
+            _check_tensor("positions", positions, torch.int32, (n,))
+        _check_device(kv.device, x=x, kv=kv, slots=slots, kv_row_scale=kv_row_scale, page_table=page_table, seq=seq,
+                      norm_weight=norm_weight, positions=positions)
+        B, pps = (0, 0) if page_table is None else page_table.shape
+        self.shape = AppendShape(n, x.stride(0) if n > 1 else width, kv.shape[0] * (64 if kind == KV_DSV4_PAGED else 1),
+                                 DTYPES[x.dtype], kind, page_size, pps, B, eps, 0)
+        self._ready(kv.device, (ctypes.byref(self.shape), _ptr(x), _ptr(norm_weight),
+                                None if rope is None else ctypes.byref(rope.data), _ptr(positions), _ptr(slots),
+                                _ptr(seq), _ptr(page_table), _ptr(kv), _ptr(kv_row_scale)),
+                    (x, kv, slots, kv_row_scale, page_table, seq, norm_weight, rope, positions))
+
+
+def cache_append(x, kv, slots, *, kv_row_scale=None, page_table=None, page_size: int = 0, seq=None, norm_weight=None,
+                 eps: float = 1e-6, rope: RopeTable | None = None, positions=None):
+    """Writes the rows x [n, 576] ([n, 512] for DeepSeek-V4 pages) of n new
+    tokens into the cache ``kv``: RMS norm of the first 512 dims (with
+    ``norm_weight`` [512] fp32), rotation of the last 64 by ``positions`` (with
+    ``rope``, a 64-dim table), encoding in the cache's layout.  slots [n] int32:
+    physical rows (flat pool), or logical positions of the token's sequence
+    (paged); negative: skipped.  seq [n] int32 names the sequences; without
+    it the tokens are equal runs, sequence by sequence."""
+    CacheAppendPlan(x, kv, slots, kv_row_scale=kv_row_scale, page_table=page_table, page_size=page_size, seq=seq,
+                    norm_weight=norm_weight, eps=eps, rope=rope, positions=positions).run()
+
+
+# ------------------------------------------------------- attention weights
+class AttentionWeightsPlan(_Plan):
+    """attention_weights() with its arguments marshalled once; the result is
+    ``out``."""
+
+    _call = "sparse_mla_attn_weights"
+
+    def __init__(self, q, kv, indices, lse, scale: float, *, kv_row_scale=None, page_table=None, page_size: int = 0,
+                 out=None):
+        _check_inputs(q, kv, indices, kv_row_scale, page_table, page_size)
+        _check_cache(kv, kv_row_scale)
+        _check_tensor("lse", lse, torch.float32, q.shape[:-1])
+        if page_table is not None and (page_table.dim() != 2 or page_table.shape[0] != q.shape[0]):
+            raise ValueError("page_table must be [B, pages_per_seq]")
+        if out is None:
+            out = torch.empty(indices.shape, dtype=torch.float32, device=q.device)
+        _check_tensor("out", out, torch.float32, indices.shape)
+        _check_device(q.device, q=q, kv=kv, indices=indices, lse=lse, kv_row_scale=kv_row_scale, page_table=page_table,
+                      out=out)
+        self.out = out
+        self.shape = shape_for(q, kv, indices, page_table=page_table, page_size=page_size)
+        self._ready(q.device, (ctypes.byref(self.shape), _ptr(q), _ptr(kv), _ptr(kv_row_scale),
+                               _ptr(page_table) if page_size else None, _ptr(indices), _ptr(lse), float(scale),
+                               _ptr(out)),
+                    (q, kv, indices, lse, kv_row_scale, page_table, out))
+
+
+def attention_weights(q, kv, indices, lse, scale: float, *, kv_row_scale=None, page_table=None, page_size: int = 0,
+                      out=None):
+    """The attention each listed row received in the decode that returned
+    ``lse``, summed over the heads: float32 of indices' shape, 0 for padding.
+    Arguments as for decode()."""
+    plan = AttentionWeightsPlan(q, kv, indices, lse, scale, kv_row_scale=kv_row_scale, page_table=page_table,
+                                page_size=page_size, out=out)
+    plan.run()
+    return plan.out
+
+
+class AccumulateWeightsPlan(_Plan):
+    """accumulate_weights() with its arguments marshalled once."""
+
+    _call = "sparse_mla_accumulate_weights"
+
+    def __init__(self, acc, indices, weights, *, decay: float = 1.0):
+        if acc.dtype != torch.float32 or acc.dim() != 2 or not acc.is_contiguous():
+            raise ValueError("acc must be contiguous float32 [B, max_ctx]")
+        B, max_ctx = acc.shape
+        if indices.dtype != torch.int32 or indices.dim() not in (2, 3) or indices.shape[0] != B \
+                or not indices.is_contiguous():
+            raise ValueError("indices must be contiguous int32 [B, topk] or [B, T, topk]")
+        _check_tensor("weights", weights, torch.float32, indices.shape)
+        _check_device(acc.device, acc=acc, indices=indices, weights=weights)
+        self._ready(acc.device, (B, indices.numel() // max(B, 1), max_ctx, _ptr(indices), _ptr(weights), float(decay),
+                                 _ptr(acc)), (acc, indices, weights))
+
+
+def accumulate_weights(acc, indices, weights, *, decay: float = 1.0):
+    """acc [B, max_ctx] float32 = decay * acc + the weights summed onto their
+    logical positions: indices and weights [B, topk] or [B, T, topk].  A
+    position may be listed any number of times; the result does not depend
+    on the order.  Returns acc."""
+    AccumulateWeightsPlan(acc, indices, weights, decay=decay).run()
+    return acc
+
+
+# ---------------------------------------------------------------- eviction
+class EvictPlan(_Plan):
+    """evict() with its arguments marshalled once; the results are ``kept``,
+    ``new_len`` and ``acc_out``."""
+
+    _call = "sparse_mla_evict"
+
+    def __init__(self, acc, ctx_len, budget: int, *, page_table, kv, kv_row_scale=None, k_cache=None, sinks: int = 0,
+                 recent: int = 0, new_page_table=None, kept=None, new_len=None, acc_out=None):
+        kind = _check_cache(kv, kv_row_scale)
+        if acc.dtype != torch.float32 or acc.dim() != 2 or not acc.is_contiguous():
+            raise ValueError("acc must be contiguous float32 [B, max_ctx]")
+        B, max_ctx = acc.shape
+        dev = acc.device
+        for name, t in (("page_table", page_table), ("new_page_table", new_page_table)):
+            if t is not None and (t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous int32 [B, pages_per_seq]")
+        if k_cache is not None and (k_cache.dtype != torch.bfloat16 or k_cache.dim() != 2
+                                    or k_cache.shape[1] != IX_DIM or not k_cache.is_contiguous()):
+            raise ValueError("k_cache must be contiguous bf16 [rows, 128]")
+        if kept is None:
+            kept = torch.empty((B, max(budget, 0)), dtype=torch.int32, device=dev)
+        if new_len is None:
+            new_len = torch.empty_like(ctx_len)
+        if acc_out is None:
+            acc_out = acc
+        _check_tensor("ctx_len", ctx_len, torch.int32, (B,))
+        _check_tensor("new_len", new_len, torch.int32, (B,))
+        _check_tensor("kept", kept, torch.int32, (B, budget))
+        _check_tensor("acc_out", acc_out, torch.float32, (B, max_ctx))
+        _check_device(dev, acc=acc, ctx_len=ctx_len, page_table=page_table, kv=kv, kv_row_scale=kv_row_scale,
+                      k_cache=k_cache, new_page_table=new_page_table, kept=kept, new_len=new_len, acc_out=acc_out)
+        self.kept, self.new_len, self.acc_out = kept, new_len, acc_out
+        self.shape = EvictShape(B, max_ctx, budget, sinks, recent, kind, page_table.shape[1],
+                                0 if new_page_table is None else new_page_table.shape[1],
+                                kv.shape[0] * (64 if kind == KV_DSV4_PAGED else 1),
+                                0 if k_cache is None else k_cache.shape[0])
+        self._ready(dev, (ctypes.byref(self.shape), _ptr(acc), _ptr(ctx_len), _ptr(kept), _ptr(new_len), _ptr(acc_out),
+                          _ptr(page_table), _ptr(new_page_table), _ptr(kv), _ptr(kv_row_scale), _ptr(k_cache)),
+                    (acc, ctx_len, page_table, kv, kv_row_scale, k_cache, new_page_table, kept, new_len, acc_out))
+
+
+def evict(acc, ctx_len, budget: int, *, page_table, kv, kv_row_scale=None, k_cache=None, sinks: int = 0,
+          recent: int = 0, new_page_table=None, kept=None, new_len=None, acc_out=None):
+    """Keeps at most ``budget`` positions of each sequence -- the first
+    ``sinks``, the last ``recent`` and those with the largest acc [B, max_ctx] --
+    and compacts the paged caches (kv, kv_row_scale, k_cache) to them, in place
+    or into the pages of ``new_page_table``.  Returns (kept [B, budget] int32,
+    -1 after the last, new_len [B] int32, acc_out), acc_out being acc unless
+    given; new_len may be given as ctx_len."""
+    plan = EvictPlan(acc, ctx_len, budget, page_table=page_table, kv=kv, kv_row_scale=kv_row_scale, k_cache=k_cache,
+                     sinks=sinks, recent=recent, new_page_table=new_page_table, kept=kept, new_len=new_len,
+                     acc_out=acc_out)
+    plan.run()
+    return plan.kept, plan.new_len, plan.acc_out

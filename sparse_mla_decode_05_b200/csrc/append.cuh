@@ -1,0 +1,290 @@
+// Cache append: new tokens' rows, normalised, rotated and encoded, into the
+// cache layouts that the decode reads.  Included by sparse_mla.cu after
+// rope.cuh (same translation unit).
+//
+// One token (row x of 576 dims; 512 for DeepSeek-V4 pages):
+//   x[0:512]  -> w x / sqrt(mean(x[0:512]^2) + eps)        (with a weight)
+//   last 64   -> turned by the token's position             (with a table)
+//   row       -> bf16, or e4m3 codes with the row scale amax / 448, or
+//                DeepSeek-V4: 448 e4m3 codes with a power-of-two scale per
+//                64 dims, then 64 bf16 dims
+// All of it in fp32 with one rounding at the end (the scale is a rounding of
+// its own): the row is read once and written once.
+
+namespace smla {
+
+constexpr int kApWarps = 4;            // warps per CTA, one token per warp at a time
+
+static_assert(sizeof(smla_append_shape) == 56 && offsetof(smla_append_shape, x_dtype) == 24, "smla_append_shape layout");
+
+struct AppendParams {
+  const void* x;
+  const float* norm_weight;       // [512] or null
+  const int32_t* positions;       // [tokens] (with a rotation)
+  const int32_t* slots;           // [tokens]
+  const int32_t* seq;             // [tokens] or null
+  const int32_t* page_table;      // [batch, pages_per_seq] (paged)
+  uint8_t* kv;
+  float* kv_row_scale;
+  long long tokens, x_stride, num_kv_rows;
+  int page_size, pages_per_seq, batch, tok_per_seq;
+  float eps;
+  int rotate;
+  smla_rope_table table;
+};
+
+// eight consecutive elements as fp32
+template <typename T, bool kVec>
+__device__ __forceinline__ void ap_load8(const T* src, float (&v)[8]) {
+  if constexpr (!kVec) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = RopeIo<T>::get(src[i]);
+  } else if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(src), b = *(reinterpret_cast<const float4*>(src) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const RopeVec<T, 8> a = *reinterpret_cast<const RopeVec<T, 8>*>(src);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = RopeIo<T>::get(a.v[i]);
+  }
+}
+// eight fp32 -> eight e4m3 codes
+__device__ __forceinline__ uint2 ap_codes8(const float (&v)[8]) {
+  return make_uint2(pack_e4m3x2(v[0], v[1]) | (pack_e4m3x2(v[2], v[3]) << 16),
+                    pack_e4m3x2(v[4], v[5]) | (pack_e4m3x2(v[6], v[7]) << 16));
+}
+__device__ __forceinline__ float ap_amax8(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+// The UE8M0 byte of a group: the smallest e with amax <= 448 * 2^(e - 127),
+// at least 1.  amax = 1.m * 2^k and 448 = 1.75 * 2^8, so e - 127 is k - 8
+// while the significand is at most 1.75 and k - 7 above it.
+__device__ __forceinline__ uint32_t ap_ue8m0(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return (uint32_t)(e < 1 ? 1 : (e > 254 ? 254 : e));
+}
+
+// One warp per token.  Lane l holds dims 8 l .. 8 l + 7 and 256 + 8 l .. +7
+// of the 512 normalised dims, and pair l of the 64 rotated ones (loaded on
+// its own: for DeepSeek-V4 pages those are dims 448 - 511, which lanes 24 -
+// 31 hold too for the mean square).  A group of 64 dims is eight lanes.
+template <typename T, int kKind, bool kVec>
+__global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr bool kDsv4 = kKind == kKindDsv4;
+  constexpr int kR = kDsv4 ? 448 : 512;                // first rotated dim
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const bool inter = p.table.layout == SMLA_ROPE_INTERLEAVED;
+  const int da = kR + (inter ? 2 * lane : lane), db = inter ? da + 1 : da + 32;
+  const long long step = (long long)gridDim.x * kApWarps;
+  for (long long i = (long long)blockIdx.x * kApWarps + (threadIdx.x >> 5); i < p.tokens; i += step) {
+    // the row: slots are physical rows, or positions through the page table
+    // of the token's sequence, as the decode's index entries are
+    const int slot = __ldg(p.slots + i);
+    long long row = slot;
+    if (slot < 0) continue;                            // no place: nothing is written
+    if (p.page_size) {
+      const long long b = p.seq ? (long long)__ldg(p.seq + i) : i / p.tok_per_seq;
+      row = -1;
+      if (b >= 0 && b < p.batch && (slot >> 6) < p.pages_per_seq) {
+        const int page = __ldg(p.page_table + b * p.pages_per_seq + (slot >> 6));
+        if (page >= 0) row = (long long)page * 64 + (slot & 63);
+      }
+    }
+    if (row < 0 || row >= p.num_kv_rows) {
+      if (lane == 0) atomicOr(&g_error_word, 4u);
+      continue;
+    }
+    const T* x = static_cast<const T*>(p.x) + i * p.x_stride;
+    float v0[8], v1[8];
+    ap_load8<T, kVec>(x + 8 * lane, v0);
+    ap_load8<T, kVec>(x + 256 + 8 * lane, v1);
+    float a = RopeIo<T>::get(x[da]), b = RopeIo<T>::get(x[db]);
+    if (p.norm_weight) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v0[j], v0[j], fmaf(v1[j], v1[j], ss));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = rsqrtf(ss * (1.0f / 512.0f) + p.eps);
+      float w0[8], w1[8];
+      ap_load8<float, true>(p.norm_weight + 8 * lane, w0);
+      ap_load8<float, true>(p.norm_weight + 256 + 8 * lane, w1);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v0[j] = v0[j] * r * w0[j];
+        v1[j] = v1[j] * r * w1[j];
+      }
+      if (kDsv4) {
+        a = a * r * __ldg(p.norm_weight + da);
+        b = b * r * __ldg(p.norm_weight + db);
+      }
+    }
+    if (p.rotate) {
+      float c, s;
+      rope_sincos(p.table.step[lane], __ldg(p.positions + i), p.table.mscale, c, s);
+      const float ra = fmaf(a, c, -b * s);
+      b = fmaf(a, s, b * c);
+      a = ra;
+    }
+    if constexpr (kKind == kKindBf16) {
+      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.kv) + row * kDqk;
+      *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
+                                                             pack_bf16x2(v0[4], v0[5]), pack_bf16x2(v0[6], v0[7]));
+      *reinterpret_cast<uint4*>(dst + 256 + 8 * lane) = make_uint4(
+          pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3]), pack_bf16x2(v1[4], v1[5]), pack_bf16x2(v1[6], v1[7]));
+      dst[da] = __float2bfloat16_rn(a);
+      dst[db] = __float2bfloat16_rn(b);
+    } else if constexpr (kKind == kKindFp8) {
+      float m = fmaxf(fmaxf(ap_amax8(v0), ap_amax8(v1)), fmaxf(fabsf(a), fabsf(b)));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      // a row of zeros keeps scale 1; a scale below the normal range would
+      // lose bits, so it stops at 2^-126
+      const float scale = m > 0.f ? fmaxf(__fdiv_rn(m, 448.0f), 1.1754943508222875e-38f) : 1.0f;
+      uint8_t* dst = p.kv + row * kRowBytesFp8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v0[j] = __fdiv_rn(v0[j], scale);
+        v1[j] = __fdiv_rn(v1[j], scale);
+      }
+      *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
+      *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
+      const uint32_t ab = pack_e4m3x2(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
+      dst[da] = (uint8_t)ab;
+      dst[db] = (uint8_t)(ab >> 8);
+      if (lane == 0) p.kv_row_scale[row] = scale;
+    } else {
+      // groups 0-3 are lanes 8 g .. 8 g + 7 of v0, groups 4-6 those of v1
+      float m0 = ap_amax8(v0), m1 = ap_amax8(v1);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+      }
+      const uint32_t e0 = ap_ue8m0(m0), e1 = ap_ue8m0(m1);
+      // division by 2^(e - 127): exact, as a product with 2^(127 - e) in two
+      // factors that are both normal
+      auto down = [](float (&v)[8], uint32_t e) {
+        const int k = 127 - (int)e, k0 = k / 2;
+        const float f0 = pow2i(k0), f1 = pow2i(k - k0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * f0 * f1;
+      };
+      down(v0, e0);
+      down(v1, e1);
+      uint8_t* page = p.kv + (row >> 6) * (long long)kDsv4Page;
+      uint8_t* dst = page + (row & 63) * kDsv4Slot;
+      *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
+      if (lane < 24) *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
+      __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(dst + kDsv4Nope);
+      rope[da - kR] = __float2bfloat16_rn(a);
+      rope[db - kR] = __float2bfloat16_rn(b);
+      uint2 block = make_uint2(0u, 0u);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        block.x |= __shfl_sync(0xffffffffu, e0, 8 * g) << (8 * g);
+        if (g < 3) block.y |= __shfl_sync(0xffffffffu, e1, 8 * g) << (8 * g);
+      }
+      if (lane == 0) *reinterpret_cast<uint2*>(page + kDsv4ScaleOff + (row & 63) * 8) = block;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host
+template <typename T, int kKind>
+static cudaError_t launch_append(AppendParams& p, bool vec, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  // resident warps: 16 CTAs of four warps per SM; more tokens loop
+  const long long ctas = (p.tokens + kApWarps - 1) / kApWarps, most = 16ll * sms;
+  void* args[] = {&p};
+  const void* kern = vec ? (const void*)smla_append_kernel<T, kKind, true> : (const void*)smla_append_kernel<T, kKind, false>;
+  return launch_pdl(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kApWarps * 32), 0, stream, args);
+}
+template <typename T>
+static cudaError_t launch_append_kind(AppendParams& p, int kv_dtype, bool vec, cudaStream_t stream) {
+  if (kv_dtype == SMLA_KV_BF16) return launch_append<T, kKindBf16>(p, vec, stream);
+  if (kv_dtype == SMLA_KV_FP8_E4M3_ROWSCALE) return launch_append<T, kKindFp8>(p, vec, stream);
+  return launch_append<T, kKindDsv4>(p, vec, stream);
+}
+
+static smla_status run_append(const smla_append_shape* s, const void* x, const float* norm_weight,
+                              const smla_rope_table* table, const int32_t* positions, const int32_t* slots,
+                              const int32_t* seq, const int32_t* page_table, void* kv, float* kv_row_scale,
+                              cudaStream_t stream) {
+  if (!s) return SMLA_ERR_INVALID_ARG;
+  const bool fp8 = s->kv_dtype == SMLA_KV_FP8_E4M3_ROWSCALE, dsv4 = s->kv_dtype == SMLA_KV_DSV4_PAGED;
+  if (s->kv_dtype != SMLA_KV_BF16 && !fp8 && !dsv4) return SMLA_ERR_UNSUPPORTED;
+  if (s->x_dtype < SMLA_DTYPE_BF16 || s->x_dtype > SMLA_DTYPE_FP32) return SMLA_ERR_UNSUPPORTED;
+  if (s->page_size != 0 && s->page_size != 64) return SMLA_ERR_UNSUPPORTED;
+  if (s->num_kv_rows < 1 || s->num_kv_rows > 0x7FFFFFFFLL) return SMLA_ERR_INVALID_ARG;
+  if (dsv4 && (s->page_size != 64 || s->num_kv_rows % 64 != 0)) return SMLA_ERR_UNSUPPORTED;
+  if (s->tokens < 0 || s->tokens > 0x7FFFFFFFLL || s->reserved != 0) return SMLA_ERR_INVALID_ARG;
+  const int width = dsv4 ? kDv : kDqk;
+  if (s->tokens > 1 && s->x_stride != 0 && s->x_stride < width) return SMLA_ERR_INVALID_ARG;
+  if (!(s->eps >= 0) || isinf(s->eps)) return SMLA_ERR_INVALID_ARG;
+  if (table) {
+    const smla_status st = validate_rope_table(table);
+    if (st != SMLA_OK) return st;
+    if (table->rope_dim != 64) return SMLA_ERR_UNSUPPORTED;
+  }
+  if (s->page_size) {
+    if (s->pages_per_seq < 1 || s->batch < 1) return SMLA_ERR_INVALID_ARG;
+    // without a sequence per token, the tokens are shared out evenly
+    if (!seq && s->tokens % s->batch != 0) return SMLA_ERR_INVALID_ARG;
+  }
+  if (fp8 != (kv_row_scale != nullptr)) return SMLA_ERR_INVALID_ARG;
+  if (s->tokens == 0) return SMLA_OK;
+  const int size = dtype_bytes(s->x_dtype);
+  if (!x || !slots || !kv || (table && !positions) || (s->page_size && !page_table)) return SMLA_ERR_INVALID_ARG;
+  if (!aligned(x, size) || !aligned(kv, 16) || !aligned(slots, 4) || (fp8 && !aligned(kv_row_scale, 4)) ||
+      (norm_weight && !aligned(norm_weight, 16)) || (table && !aligned(positions, 4)) || (seq && !aligned(seq, 4)) ||
+      (s->page_size && !aligned(page_table, 4)))
+    return SMLA_ERR_INVALID_ARG;
+  AppendParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = x;
+  p.norm_weight = norm_weight;
+  p.positions = positions;
+  p.slots = slots;
+  p.seq = seq;
+  p.page_table = page_table;
+  p.kv = static_cast<uint8_t*>(kv);
+  p.kv_row_scale = kv_row_scale;
+  p.tokens = s->tokens;
+  p.x_stride = s->tokens > 1 ? s->x_stride : 0;
+  p.num_kv_rows = s->num_kv_rows;
+  p.page_size = s->page_size;
+  p.pages_per_seq = s->pages_per_seq;
+  p.batch = s->batch;
+  p.tok_per_seq = s->page_size && !seq ? (int)(s->tokens / s->batch) : 1;
+  p.eps = s->eps;
+  p.rotate = table != nullptr;
+  if (table) p.table = *table;
+  const bool vec = aligned(x, 16) && (p.x_stride * size) % 16 == 0;
+  cudaError_t e;
+  if (s->x_dtype == SMLA_DTYPE_BF16) e = launch_append_kind<__nv_bfloat16>(p, s->kv_dtype, vec, stream);
+  else if (s->x_dtype == SMLA_DTYPE_FP16) e = launch_append_kind<__half>(p, s->kv_dtype, vec, stream);
+  else e = launch_append_kind<float>(p, s->kv_dtype, vec, stream);
+  return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+}
+
+}  // namespace smla
+
+extern "C" {
+
+smla_status sparse_mla_cache_append(const smla_append_shape* shape, const void* x, const float* norm_weight,
+                                    const smla_rope_table* table, const int32_t* positions, const int32_t* slots,
+                                    const int32_t* seq, const int32_t* page_table, void* kv_cache,
+                                    float* kv_row_scale, void* stream) {
+  return smla::run_append(shape, x, norm_weight, table, positions, slots, seq, page_table, kv_cache, kv_row_scale,
+                          static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

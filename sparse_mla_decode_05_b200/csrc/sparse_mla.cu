@@ -2536,6 +2536,10 @@ static HostStaging host_staging(const smla_shape* s, size_t ws_bytes) {
 
 // the indexer step (scores and top-k selection), sharing the helpers above
 #include "indexer.cuh"
+#include "rope.cuh"
+#include "append.cuh"
+#include "weights.cuh"
+#include "evict.cuh"
 
 // ============================================================ C ABI
 extern "C" {
