@@ -594,6 +594,11 @@ def _check_tensor(name, t, dtype, shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
+# handle of a device's current stream, without building a Stream object for it
+# (0.1 us instead of 2.2)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 class _Plan:
     """A call with its arguments marshalled once.  run() is one call into the
     library, on the current stream of the tensors' device unless a stream is
@@ -611,13 +616,15 @@ class _Plan:
         if self._empty:
             return
         dev = self._device
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        s = s.cuda_stream if hasattr(s, "cuda_stream") else s
+        if stream is None:
+            stream = _current_stream(dev.index)
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
         if torch.cuda.current_device() == dev.index:
-            st = self._fn(*self._args, s)
+            st = self._fn(*self._args, stream)
         else:
             with torch.cuda.device(dev):
-                st = self._fn(*self._args, s)
+                st = self._fn(*self._args, stream)
         if st != 0:
             raise SmlaError(st, self._call)
 

@@ -7,21 +7,54 @@
 
 namespace smla {
 
-constexpr int kWtTile = 128;                       // entries per CTA (MMA M)
-constexpr int kWtThreads = 256;
-constexpr int kWtAtomK = kWtTile * 128;            // 64 dims of the rows: 128 rows x 128 B
-constexpr int kWtAtomQ = kH * 128;                 // 64 dims of the query: 64 heads x 128 B
-constexpr int kWtSmemK = 0;
-constexpr int kWtSmemQ = kWtSmemK + kAtoms * kWtAtomK;
-constexpr int kWtSmemRow = kWtSmemQ + kAtoms * kWtAtomQ;   // int  [128] physical row or -1
-constexpr int kWtSmemScale = kWtSmemRow + kWtTile * 4;     // f32  [128] row scale
-constexpr int kWtSmemLse = kWtSmemScale + kWtTile * 4;     // f32  [64]  lse
-constexpr int kWtSmemPart = kWtSmemLse + kH * 4;           // f32  [128] the upper 32 heads' sums
-constexpr int kWtSmemBar = kWtSmemPart + kWtTile * 4;
-constexpr int kWtSmemTmem = kWtSmemBar + 8;
-constexpr int kWtSmemBytes = kWtSmemTmem + 8;
-static_assert(kWtSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory of sm_100");
-constexpr uint32_t kIdescWt = make_idesc(128, 64, false, false);
+constexpr int kWtTile = 64;                        // entries per tile (MMA M)
+constexpr int kWtEpiWarps = 8, kWtCopyWarps = 8;
+constexpr int kWtThreads = 32 * (1 + kWtEpiWarps + kWtCopyWarps);
+constexpr int kWtRing = 8;                         // tiles whose rows and scales are kept
+constexpr int kWtAtom = kWtTile * 128;             // 128 bytes of each of the 64 rows
+// Shared-memory operands are 128-byte-swizzled atoms of [rows][128 B]; the
+// last 64 bytes of a 576-byte fp8 row are a 64-byte-swizzled atom [rows][64 B].
+template <int kKind>
+struct WtCfg {
+  static constexpr bool kFp8 = kKind == kKindFp8;
+  static constexpr int kQK = kKind == kKindDsv4 ? 512 : kDqk;
+  static constexpr int kRowBytes = kFp8 ? kQK : 2 * kQK;           // of an operand row
+  static constexpr int kStages = kFp8 ? 4 : 2;
+  static constexpr int kStageBytes = kWtTile * kRowBytes;
+  static constexpr int kQRows = kFp8 ? 128 : 64;                   // fp8: the heads' high parts, then their low parts
+  static constexpr int kQBytes = kQRows * kRowBytes;
+  static constexpr int kN = kQRows;                                // MMA N: columns of a score buffer
+  static constexpr uint32_t kTmem = 2 * kN;
+  static constexpr int kSmemQ = kStages * kStageBytes;
+  static constexpr int kSmemRow = kSmemQ + kQBytes;                // int  [kWtRing][64] physical row or -1
+  static constexpr int kSmemScale = kSmemRow + kWtRing * 64 * 4;   // f32  [kWtRing][64] row scale (fp8)
+  static constexpr int kSmemLse = kSmemScale + kWtRing * 64 * 4;   // f32  [2][64] by row parity
+  static constexpr int kSmemK = kSmemLse + 2 * 64 * 4;             // f32  [2][64] scale, over the query's power of two
+  static constexpr int kSmemBar = kSmemK + 2 * 64 * 4;
+  static constexpr int kSmemTmem = kSmemBar + 8 * 16;
+  static constexpr int kSmemBytes = kSmemTmem + 16;
+  static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory of sm_100");
+  static_assert(kSmemQ % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled operands need 1024-byte aligned atoms");
+  // Reuse of the row / scale ring: tile t + stages + 2 is copied after MMA(t + 2) has completed, which waited for
+  // the epilogue of tile t to have read its slot.
+  static_assert(kWtRing >= kStages + 2, "row ring");
+};
+constexpr uint32_t kIdescWt = make_idesc(64, 64, false, false), kIdescWt8 = make_idesc_e4m3(64, 128, false);
+// barriers
+constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13;
+
+// Shared-memory matrix descriptor, 64-byte swizzle (layout type 4), K-major:
+// rows of 64 B, 8-row groups 512 B apart.
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(512 >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+__device__ __forceinline__ uint32_t sw64_off(int r, int j) { return (uint32_t)(r * 64 + ((j ^ ((r >> 1) & 3)) << 4)); }
+// byte offset of 16-byte chunk c (0..35) of row r of a 576-byte-row operand of `rows` rows
+template <int kRows>
+__device__ __forceinline__ uint32_t wt_off8(int r, int c) {
+  return c < 32 ? (uint32_t)((c >> 3) * (kRows * 128)) + sw128_off(r, c & 7)
+                : (uint32_t)(4 * kRows * 128) + sw64_off(r, c - 32);
+}
 
 struct WeightsParams {
   const uint8_t* q;
@@ -32,6 +65,8 @@ struct WeightsParams {
   const float* lse;
   float* out;
   int topk, tok_per_seq, page_size, pages_per_seq, num_kv_rows;
+  int ntiles;                // tiles per decode row
+  long long total;           // rows x ntiles
   float scale;
 };
 
@@ -55,121 +90,350 @@ __device__ __forceinline__ int resolve_row(const P& p, int idx, int drow) {
   return (int)r;
 }
 
-// One CTA per (decode row, tile of 128 entries): rows and query into shared
-// memory as bf16 (128-byte swizzle), D[128 entries x 64 heads] = K Q^T in
-// tensor memory, then two threads per entry sum exp over 32 heads each.
+// Eight heads of a row's query (h0 .. h0 + 7) into the B operand, by one warp.
+// bf16 caches: as they are.  fp8: times the power of two that brings the
+// head's largest |q| into [128, 256), split into e4m3 high and low parts
+// (exact for the bf16 values whose parts are e4m3 normals, within 2^-10 of the
+// scaled value otherwise); s_k[h] receives scale over that power.
+template <int kKind>
+__device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* smem, uint32_t sbase, int row, int h0,
+                                               int lane, float* s_k) {
+  using C = WtCfg<kKind>;
+  constexpr int kChunks = C::kQK / 8;               // 16-byte chunks of a head
+  const uint8_t* q = p.q + ((size_t)row * kH + h0) * (C::kQK * 2);
+  const uint32_t qb = sbase + C::kSmemQ;
+  if constexpr (!C::kFp8) {
+    for (int c = lane; c < 8 * kChunks; c += 32) {
+      const int h = c / kChunks, j = c - h * kChunks;
+      cp_async_16(qb + (uint32_t)((j >> 3) * (C::kQRows * 128)) + sw128_off(h0 + h, j & 7), q + (size_t)c * 16, 16u);
+    }
+    cp_async_wait_all();
+  } else {
+    // lane l: chunks l, 32 + l and, of lanes 0-7, 64 + l; four heads at a time
+#pragma unroll 1
+    for (int hh = 0; hh < 8; hh += 4) {
+      uint4 v[4][3];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)(hh + i) * (C::kQK * 2));
+        v[i][0] = __ldg(src + lane);
+        v[i][1] = __ldg(src + 32 + lane);
+        v[i][2] = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = h0 + hh + i;
+        float m = 0.f;
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w4[k] << 16)), fabsf(__uint_as_float(w4[k] & 0xFFFF0000u))));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // 2^sq as two factors, so that both stay normal for any q
+        int sq = m > 0.f ? 7 - ilog2f(m) : 0;
+        sq = sq > 120 ? 120 : (sq < -120 ? -120 : sq);
+        const float up = pow2i(sq);
+#pragma unroll
+        for (int u = 0; u < 3; ++u) {
+          if (u == 2 && lane >= 8) continue;
+          const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            split_e4m3x2(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xFFFF0000u) * up, hi[k], lo[k]);
+          // eight codes: half of 16-byte chunk (32 u + lane) / 2 of the row
+          const int c = (32 * u + lane) >> 1;
+          const uint32_t at = (uint32_t)(8 * (lane & 1));
+          *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(h, c) + at) =
+              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(64 + h, c) + at) =
+              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        }
+        if (lane == 0) s_k[h] = p.scale * pow2i(-sq);
+      }
+    }
+  }
+}
+
+// The decode rows' tiles of 64 entries are laid end to end and shared out
+// evenly over one CTA per SM; every tile's weights are its own, so nothing is
+// merged.  Warp roles: one MMA issuer; eight epilogue warps, which also
+// stage the query of each row the CTA meets; eight copy warps.
+//  * Copy warp w resolves and gathers rows 8 w .. 8 w + 7 of each tile by
+//    16-byte cp.async (lane = chunk of one row, the rows' last 64 bytes
+//    merged): conflict-free in the swizzled atoms, two to four tiles ahead.
+//  * S[64 entries x 64 heads] = K Q^T in tensor memory, two buffers.  fp8 rows
+//    are multiplied as stored (kind::f8f6f4) by the query scaled per head by
+//    a power of two and split into e4m3 high and low parts, as in the decode:
+//    columns 0-63 and 64-127 of the buffer.
+//  * Epilogue warps 0-3 take the even tiles, 4-7 the odd ones; a thread has one
+//    entry and 32 heads, the other 32 are its partner's, sixteen lanes on.
 template <int kKind>
 __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __grid_constant__ WeightsParams p) {
-  constexpr bool kDsv4 = kKind == kKindDsv4, kFp8 = kKind == kKindFp8;
-  constexpr int kQK = kDsv4 ? 512 : kDqk;
-  constexpr int kQAtoms = kQK / 64;
+  using C = WtCfg<kKind>;
+  constexpr bool kFp8 = C::kFp8, kDsv4 = kKind == kKindDsv4;
+  constexpr int kStages = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const int drow = blockIdx.y, e0 = blockIdx.x * kWtTile;
-  const uint32_t bar = sbase + kWtSmemBar;
-  grid_dep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto BAR = [&](int i) -> uint32_t { return sbase + C::kSmemBar + 8u * (uint32_t)i; };
   if (sbase & 1023u) {
-    if (t == 0) atomicOr(&g_error_word, 2u);
+    grid_dep_wait();
+    if (threadIdx.x == 0) atomicOr(&g_error_word, 2u);
     return;
   }
-  if (t == 0) {
-    mbar_init(bar, 1);
+  // this CTA's tiles
+  const int nt = p.ntiles;
+  const long long g0 = (long long)blockIdx.x * p.total / gridDim.x, g1 = (long long)(blockIdx.x + 1) * p.total / gridDim.x;
+  const int count = (int)(g1 - g0);
+  const int row0 = (int)(g0 / nt), tin0 = (int)(g0 % nt);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      // a copying thread's copies (fp8, bf16), and each copy warp's row numbers or converted rows
+      mbar_init(BAR(WB_FULL + i), kWtCopyWarps + (kDsv4 ? 0 : 32 * kWtCopyWarps));
+      mbar_init(BAR(WB_EMPTY + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(BAR(WB_SF + i), 1);
+      mbar_init(BAR(WB_SE + i), kWtEpiWarps / 2);
+    }
+    mbar_init(BAR(WB_Q), kWtEpiWarps);
+    mbar_init(BAR(WB_FIN), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
-    tmem_alloc(sbase + kWtSmemTmem, 64);
+    tmem_alloc(sbase + C::kSmemTmem, C::kTmem);
     tmem_relinquish();
   }
-  int* s_row = reinterpret_cast<int*>(smem + kWtSmemRow);
-  float* s_scale = reinterpret_cast<float*>(smem + kWtSmemScale);
-  float* s_lse = reinterpret_cast<float*>(smem + kWtSmemLse);
-  float* s_part = reinterpret_cast<float*>(smem + kWtSmemPart);
-  if (t < kWtTile) {
-    const int idx = e0 + t < p.topk ? __ldg(p.indices + (size_t)drow * p.topk + e0 + t) : -1;
-    const int r = resolve_row(p, idx, drow);
-    s_row[t] = r;
-    s_scale[t] = kFp8 && r >= 0 ? __ldg(p.kv_row_scale + r) : 1.f;
-  } else if (t < kWtTile + kH) {
-    // a head without any valid entry has lse -inf and takes no part
-    const float l = __ldg(p.lse + (size_t)drow * kH + t - kWtTile);
-    s_lse[t - kWtTile] = l == -INFINITY ? INFINITY : l;
-  }
-  const uint8_t* q = p.q + (size_t)drow * kH * kQK * 2;
-  for (int c = t; c < kH * kQK / 8; c += kWtThreads) {
-    const int h = c / (kQK / 8), j = c % (kQK / 8);
-    cp_async_16(sbase + kWtSmemQ + (j >> 3) * kWtAtomQ + sw128_off(h, j & 7), q + (size_t)c * 16, 16u);
-  }
+  tc_fence_before();
   __syncthreads();
-  if constexpr (kKind == kKindBf16) {
-    for (int c = t; c < kWtTile * (kQK / 8); c += kWtThreads) {
-      const int e = c / (kQK / 8), j = c % (kQK / 8);
-      const int r = s_row[e];
-      cp_async_16(sbase + kWtSmemK + (j >> 3) * kWtAtomK + sw128_off(e, j & 7),
-                  p.kv + (size_t)(r >= 0 ? r : 0) * kRowBytesBf16 + j * 16, r >= 0 ? 16u : 0u);
+  tc_fence_after();
+  grid_dep_wait();
+  grid_dep_launch();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kSmemTmem);
+  int* s_row = reinterpret_cast<int*>(smem + C::kSmemRow);
+  float* s_scale = reinterpret_cast<float*>(smem + C::kSmemScale);
+  float* s_lse = reinterpret_cast<float*>(smem + C::kSmemLse);
+  float* s_k = reinterpret_cast<float*>(smem + C::kSmemK);
+  auto wait_all = [&](int bar, int parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(BAR(bar), (uint32_t)parity));
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ MMA issuer
+    bool ok = true;
+    int tin = tin0, seg = 0;
+    for (int t = 0; ok && t < count; ++t, tin = tin + 1 == nt ? 0 : tin + 1) {
+      const int stage = t % kStages, buf = t & 1;
+      if (t == 0 || tin == 0) ok = wait_all(WB_Q, seg++ & 1);
+      if (ok && t >= 2) ok = wait_all(WB_SE + buf, ((t >> 1) - 1) & 1);
+      if (ok) ok = wait_all(WB_FULL + stage, (t / kStages) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      fence_proxy_async_smem();    // the copies (generic proxy) before the tensor core's reads
+      const uint32_t d = tmem + (uint32_t)(buf * C::kN);
+      const uint32_t a = sbase + (uint32_t)(stage * C::kStageBytes), b = sbase + C::kSmemQ;
+      if constexpr (kFp8) {
+        const uint32_t idesc = kIdescWt8;
+        const uint64_t da = sw128_desc(a, 16, 1024), db = sw128_desc(b, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          mma8_ss_elect(d, da + (uint64_t)((k >> 2) * (kWtAtom >> 4) + (k & 3) * 2),
+                        db + (uint64_t)((k >> 2) * (C::kQRows * 128 >> 4) + (k & 3) * 2), idesc, k > 0);
+        const uint64_t ta = sw64_desc(a + 4 * kWtAtom), tb = sw64_desc(b + 4 * C::kQRows * 128);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) mma8_ss_elect(d, ta + (uint64_t)(2 * k), tb + (uint64_t)(2 * k), idesc, true);
+      } else {
+        const uint32_t idesc = kIdescWt;
+        const uint64_t da = sw128_desc(a, 16, 1024), db = sw128_desc(b, 16, 1024);
+#pragma unroll
+        for (int k = 0; k < C::kQK / 16; ++k) {
+          const uint64_t off = (uint64_t)((k >> 2) * (kWtAtom >> 4) + (k & 3) * 2);
+          if (k == 0) mma_set_elect(d, da, db, idesc);
+          else mma_acc_elect(d, da + off, db + off, idesc);
+        }
+      }
+      commit_elect(BAR(WB_EMPTY + stage));
+      commit_elect(BAR(WB_SF + buf));
+    }
+    // every MMA issued has completed before teardown
+    commit_elect(BAR(WB_FIN));
+    mbar_wait(BAR(WB_FIN), 0);
+  } else if (warp <= kWtEpiWarps) {
+    // -------------------------------------------------------------- epilogue
+    const int ew = warp - 1, group = ew >> 2, quarter = warp & 3;
+    const int e = 16 * quarter + (lane & 15), half = lane >> 4;
+    bool ok = true;
+    int row = row0, tin = tin0, seg = 0;
+    for (int t = 0; ok && t < count; ++t) {
+      if (t == 0 || tin == 0) {
+        // the row's query, once the last row's products are done
+        if (t > 0) ok = wait_all(WB_SF + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+        if (!ok) break;
+        const int h0 = 8 * ew, sb = (seg & 1) * 64;
+        if (lane < 8) {
+          // a head without any valid entry has lse -inf and takes no part
+          const float l = __ldg(p.lse + (size_t)row * kH + h0 + lane);
+          s_lse[sb + h0 + lane] = l == -INFINITY ? INFINITY : l;
+          if (!kFp8) s_k[sb + h0 + lane] = p.scale;
+        }
+        wt_stage_query<kKind>(p, smem, sbase, row, h0, lane, s_k + sb);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(WB_Q));
+        ++seg;
+      }
+      if ((t & 1) == group) {
+        ok = wait_all(WB_SF + group, (t >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        const int rs = (t % kWtRing) * 64 + e;
+        const int r = s_row[rs];
+        const float rsc = kFp8 ? s_scale[rs] : 1.f;
+        const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(group * C::kN);
+        float x[32];
+        tmem_ld_16x32bx2_x32(d, x);
+        if constexpr (kFp8) {
+          float lo[32];
+          tmem_ld_16x32bx2_x32(d + 64, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 32; ++h) x[h] += lo[h];
+        } else {
+          tmem_wait_ld();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(WB_SE + group));
+        // scale q.k - lse in natural units and one rounding: where a weight is
+        // large the difference is small, so the exponential is taken of a
+        // number known to its own last bits, not to those of the lse
+        const float* lse = s_lse + ((seg - 1) & 1) * 64 + 32 * half;
+        const float* kh = s_k + ((seg - 1) & 1) * 64 + 32 * half;
+        float sum = 0.f;
+#pragma unroll
+        for (int h = 0; h < 32; h += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(lse + h), k4 = *reinterpret_cast<const float4*>(kh + h);
+          sum += ex2(1.44269504f * fmaf(x[h] * rsc, k4.x, -l4.x)) + ex2(1.44269504f * fmaf(x[h + 1] * rsc, k4.y, -l4.y)) +
+                 (ex2(1.44269504f * fmaf(x[h + 2] * rsc, k4.z, -l4.z)) + ex2(1.44269504f * fmaf(x[h + 3] * rsc, k4.w, -l4.w)));
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int at = tin * kWtTile + e;
+        if (half == 0 && at < p.topk) p.out[(size_t)row * p.topk + at] = r >= 0 ? sum : 0.f;
+      }
+      if (++tin == nt) {
+        tin = 0;
+        ++row;
+      }
     }
   } else {
-    // 36 chunks of 16 bytes per row: 16 codes each, or (DeepSeek-V4, from
-    // chunk 28 on) eight bf16 dims
-    for (int c = t; c < kWtTile * 36; c += kWtThreads) {
-      const int e = c / 36, j = c % 36;
-      const int r = s_row[e];
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      const uint8_t* src = kDsv4 ? p.kv + (size_t)(r >> 6) * kDsv4Page + (r & 63) * kDsv4Slot : p.kv + (size_t)r * 576;
-      if (r >= 0) v = *reinterpret_cast<const uint4*>(src + j * 16);
-      if (kDsv4 && j >= 28) {
-        st_shared_v4(sbase + kWtSmemK + 7 * kWtAtomK + sw128_off(e, j - 28), v);
-        continue;
-      }
-      uint32_t s2 = 0x3F803F80u;
-      if (kDsv4 && r >= 0)
-        s2 = ue8m0_bf16x2(p.kv[(size_t)(r >> 6) * kDsv4Page + kDsv4ScaleOff + (r & 63) * 8 + (j >> 2)]);
-      uint4 lo, hi;
-      e4m3x4_to_bf16x4_scaled(v.x, s2, lo.x, lo.y);
-      e4m3x4_to_bf16x4_scaled(v.y, s2, lo.z, lo.w);
-      e4m3x4_to_bf16x4_scaled(v.z, s2, hi.x, hi.y);
-      e4m3x4_to_bf16x4_scaled(v.w, s2, hi.z, hi.w);
-      const uint32_t atom = sbase + kWtSmemK + (j >> 2) * kWtAtomK;
-      st_shared_v4(atom + sw128_off(e, 2 * (j & 3)), lo);
-      st_shared_v4(atom + sw128_off(e, 2 * (j & 3) + 1), hi);
-    }
-  }
-  cp_async_wait_all();
-  fence_proxy_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kWtSmemTmem);
-  if (warp == 0) {
-    const uint64_t da = sw128_desc(sbase + kWtSmemK, 16, 1024), db = sw128_desc(sbase + kWtSmemQ, 16, 1024);
-    for (int ks = 0; ks < kQK / 16; ++ks) {
-      const uint64_t ao = (uint64_t)((ks >> 2) * (kWtAtomK >> 4) + (ks & 3) * 2);
-      const uint64_t bo = (uint64_t)((ks >> 2) * (kWtAtomQ >> 4) + (ks & 3) * 2);
-      if (ks == 0) mma_set_elect(tmem, da + ao, db + bo, kIdescWt);
-      else mma_acc_elect(tmem, da + ao, db + bo, kIdescWt);
-    }
-    commit_elect(bar);
-  }
-  const bool ok = mbar_wait(bar, 0);
-  tc_fence_after();
-  const int e = (warp & 3) * 32 + lane, half = warp >> 2;
-  float sum = 0.f;
-  if (ok) {
-    float x[32];
-    tmem_ld_32x32b_x32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 32u * (uint32_t)half, x);
-    tmem_wait_ld();
-    // scale q.k - lse in one rounding, in natural units: where a weight is
-    // large the difference is small, so what the exponential is taken of is
-    // known to its own last bits, not to those of the lse
-    const float k = p.scale * s_scale[e];
+    // ------------------------------------------------------------- copy warps
+    const int cw = warp - 1 - kWtEpiWarps, r8 = lane & 7;
+    // lanes l, l + 8, ... hold row 8 cw + l of a tile: entry of tile t + 2,
+    // row of tile t + 1, and tile t's row being copied
+    struct Cursor {
+      int row, tin;
+    };
+    Cursor c1{row0, tin0};
+    auto next = [&](Cursor c) -> Cursor { return c.tin + 1 == nt ? Cursor{c.row + 1, 0} : Cursor{c.row, c.tin + 1}; };
+    auto entry = [&](Cursor c, int t) -> int {
+      const int at = c.tin * kWtTile + 8 * cw + r8;
+      return t < count && at < p.topk ? __ldg(p.indices + (size_t)c.row * p.topk + at) : -1;
+    };
+    int r0 = resolve_row(p, entry(c1, 0), row0);
+    c1 = next(c1);
+    int i1 = entry(c1, 1);
+    for (int t = 0; t < count; ++t) {
+      const int stage = t % kStages, rs = (t % kWtRing) * 64;
+      const int r1 = resolve_row(p, i1, c1.row);
+      c1 = next(c1);
+      i1 = entry(c1, t + 2);
+      const uint32_t base = sbase + (uint32_t)(stage * C::kStageBytes);
+      if constexpr (kDsv4) {
+        // codes to bf16 on the way: the loads first, then the stage's turn
+        uint4 v[9];
+        uint2 dsc[9];
 #pragma unroll
-    for (int h = 0; h < 32; ++h) sum += ex2(1.44269504f * fmaf(x[h], k, -s_lse[32 * half + h]));
+        for (int u = 0; u < 9; ++u) {
+          const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr;      // chunk j of the warp's row rr
+          const int r = __shfl_sync(0xffffffffu, r0, rr);
+          v[u] = make_uint4(0u, 0u, 0u, 0u);
+          dsc[u] = make_uint2(0u, 0u);
+          if (r >= 0) {
+            const uint8_t* page = p.kv + (size_t)(r >> 6) * kDsv4Page;
+            v[u] = __ldg(reinterpret_cast<const uint4*>(page + (r & 63) * kDsv4Slot + 16 * j));
+            dsc[u] = __ldg(reinterpret_cast<const uint2*>(page + kDsv4ScaleOff + (r & 63) * 8));
+          }
+        }
+        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
+#pragma unroll
+        for (int u = 0; u < 9; ++u) {
+          const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr, tok = 8 * cw + rr;
+          if (j >= 28) {
+            st_shared_v4(base + 7 * kWtAtom + sw128_off(tok, j - 28), v[u]);
+          } else {
+            const int g = j >> 2;
+            const uint32_t s2 = ue8m0_bf16x2(((g < 4 ? dsc[u].x : dsc[u].y) >> (8 * (g & 3))) & 0xFFu);
+            uint4 lo, hi;
+            e4m3x4_to_bf16x4_scaled(v[u].x, s2, lo.x, lo.y);
+            e4m3x4_to_bf16x4_scaled(v[u].y, s2, lo.z, lo.w);
+            e4m3x4_to_bf16x4_scaled(v[u].z, s2, hi.x, hi.y);
+            e4m3x4_to_bf16x4_scaled(v[u].w, s2, hi.z, hi.w);
+            st_shared_v4(base + g * kWtAtom + sw128_off(tok, 2 * (j & 3)), lo);
+            st_shared_v4(base + g * kWtAtom + sw128_off(tok, 2 * (j & 3) + 1), hi);
+          }
+        }
+        if (lane < 8) s_row[rs + 8 * cw + lane] = r0;
+        fence_proxy_async_smem();
+      } else {
+        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
+        // one instruction per row and 512 bytes, then the eight rows' tails
+        // together.  Absent rows read nothing and are zero.
+#pragma unroll
+        for (int rr = 0; rr < 8; ++rr) {
+          const int r = __shfl_sync(0xffffffffu, r0, rr);
+          const uint32_t n = r >= 0 ? 16u : 0u;
+          const uint8_t* src = p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + lane * 16;
+          if constexpr (kFp8) {
+            cp_async_16(base + wt_off8<kWtTile>(8 * cw + rr, lane), src, n);
+          } else {
+            const uint32_t at = base + (uint32_t)((lane >> 3) * kWtAtom) + sw128_off(8 * cw + rr, lane & 7);
+            cp_async_16(at, src, n);
+            cp_async_16(at + 4 * kWtAtom, src + 512, n);
+          }
+        }
+        if constexpr (kFp8) {
+          const int rr = lane >> 2, r = __shfl_sync(0xffffffffu, r0, rr);
+          cp_async_16(base + wt_off8<kWtTile>(8 * cw + rr, 32 + (lane & 3)),
+                      p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 512 + (lane & 3) * 16, r >= 0 ? 16u : 0u);
+          // the row's scale rides along (a copy of four bytes)
+          if (lane < 8)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_scale + rs + 8 * cw + lane)),
+                         "l"(p.kv_row_scale + (r0 >= 0 ? r0 : 0)) : "memory");
+        } else {
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int rr = 4 * hh + (lane >> 3), r = __shfl_sync(0xffffffffu, r0, rr);
+            cp_async_16(base + 8 * kWtAtom + sw128_off(8 * cw + rr, lane & 7),
+                        p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 1024 + (lane & 7) * 16, r >= 0 ? 16u : 0u);
+          }
+        }
+        if (lane < 8) s_row[rs + 8 * cw + lane] = r0;
+        cp_async_mbar_arrive_noinc(BAR(WB_FULL + stage));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(WB_FULL + stage));
+      r0 = r1;
+    }
+    cp_async_wait_all();
   }
-  if (half) s_part[e] = sum;
   tc_fence_before();
   __syncthreads();
-  if (!half && e0 + e < p.topk) p.out[(size_t)drow * p.topk + e0 + e] = s_row[e] >= 0 ? sum + s_part[e] : 0.f;
-  if (warp == 0) tmem_dealloc(tmem, 64);
+  if (warp == 0) tmem_dealloc(tmem, C::kTmem);
 }
 
 // ---------------------------------------------------------- accumulation
@@ -242,19 +506,22 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
 
 // ------------------------------------------------------------------ host
 template <int kKind>
-static cudaError_t launch_weights(WeightsParams& p, int rows, cudaStream_t stream) {
+static cudaError_t launch_weights(WeightsParams& p, cudaStream_t stream) {
   static volatile int done[64] = {0};
+  constexpr int bytes = WtCfg<kKind>::kSmemBytes;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64 || !done[dev]) {
-    e = cudaFuncSetAttribute(smla_weights_kernel<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, kWtSmemBytes);
+    e = cudaFuncSetAttribute(smla_weights_kernel<kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) done[dev] = 1;
   }
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
   void* args[] = {&p};
-  return launch_pdl((const void*)smla_weights_kernel<kKind>, dim3((unsigned)((p.topk + kWtTile - 1) / kWtTile), (unsigned)rows),
-                    dim3(kWtThreads), kWtSmemBytes, stream, args);
+  return launch_pdl((const void*)smla_weights_kernel<kKind>, dim3((unsigned)(p.total < sms ? p.total : sms)),
+                    dim3(kWtThreads), bytes, stream, args);
 }
 
 static smla_status run_weights(const smla_shape* s, const void* q, const void* kv, const float* kv_row_scale,
@@ -283,10 +550,12 @@ static smla_status run_weights(const smla_shape* s, const void* q, const void* k
   p.page_size = s->page_size;
   p.pages_per_seq = s->pages_per_seq;
   p.num_kv_rows = (int)s->num_kv_rows;
+  p.ntiles = (s->topk + kWtTile - 1) / kWtTile;
+  p.total = (long long)rows_of(s) * p.ntiles;
   p.scale = scale;
-  const cudaError_t e = fp8 ? launch_weights<kKindFp8>(p, rows_of(s), stream)
-                            : (s->kv_dtype == SMLA_KV_DSV4_PAGED ? launch_weights<kKindDsv4>(p, rows_of(s), stream)
-                                                                : launch_weights<kKindBf16>(p, rows_of(s), stream));
+  const cudaError_t e = fp8 ? launch_weights<kKindFp8>(p, stream)
+                            : (s->kv_dtype == SMLA_KV_DSV4_PAGED ? launch_weights<kKindDsv4>(p, stream)
+                                                                : launch_weights<kKindBf16>(p, stream));
   return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
