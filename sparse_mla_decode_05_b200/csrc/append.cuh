@@ -33,21 +33,19 @@ struct AppendParams {
   smla_rope_table table;
 };
 
-// eight consecutive elements as fp32
+// eight consecutive elements, as stored
 template <typename T, bool kVec>
-__device__ __forceinline__ void ap_load8(const T* src, float (&v)[8]) {
+__device__ __forceinline__ RopeVec<T, 8> ap_load8(const T* src) {
+  RopeVec<T, 8> r;
   if constexpr (!kVec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = RopeIo<T>::get(src[i]);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(src), b = *(reinterpret_cast<const float4*>(src) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    for (int i = 0; i < 8; ++i) r.v[i] = src[i];
   } else {
-    const RopeVec<T, 8> a = *reinterpret_cast<const RopeVec<T, 8>*>(src);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = RopeIo<T>::get(a.v[i]);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      reinterpret_cast<uint4*>(&r)[i] = reinterpret_cast<const uint4*>(src)[i];
   }
+  return r;
 }
 // eight fp32 -> eight e4m3 codes
 __device__ __forceinline__ uint2 ap_codes8(const float (&v)[8]) {
@@ -81,30 +79,64 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
   const int lane = threadIdx.x & 31;
   const bool inter = p.table.layout == SMLA_ROPE_INTERLEAVED;
   const int da = kR + (inter ? 2 * lane : lane), db = inter ? da + 1 : da + 32;
-  const long long step = (long long)gridDim.x * kApWarps;
-  for (long long i = (long long)blockIdx.x * kApWarps + (threadIdx.x >> 5); i < p.tokens; i += step) {
-    // the row: slots are physical rows, or positions through the page table
-    // of the token's sequence, as the decode's index entries are
-    const int slot = __ldg(p.slots + i);
-    long long row = slot;
-    if (slot < 0) continue;                            // no place: nothing is written
-    if (p.page_size) {
-      const long long b = p.seq ? (long long)__ldg(p.seq + i) : i / p.tok_per_seq;
+  const long long stride = (long long)gridDim.x * kApWarps;
+  const unsigned long long turn = p.table.step[lane];
+  float w0[8], w1[8], wa = 1.f, wb = 1.f;
+  if (p.norm_weight) {
+    rope_unpack<float, 8>(ap_load8<float, true>(p.norm_weight + 8 * lane), w0);
+    rope_unpack<float, 8>(ap_load8<float, true>(p.norm_weight + 256 + 8 * lane), w1);
+    if (kDsv4) {
+      wa = __ldg(p.norm_weight + da);
+      wb = __ldg(p.norm_weight + db);
+    }
+  }
+  // The next token's loads are issued before this one's arithmetic.  The row
+  // itself does not wait for its place: slots are physical rows, or
+  // positions through the page table of the token's sequence, as the decode's
+  // index entries are.
+  struct Token {
+    RopeVec<T, 8> v0, v1;
+    T a, b;
+    int slot, pos;
+    long long seq;
+  };
+  auto load = [&](long long i) -> Token {
+    Token k;
+    k.slot = -1;
+    if (i < p.tokens) {
+      const T* x = static_cast<const T*>(p.x) + i * p.x_stride;
+      k.slot = __ldg(p.slots + i);
+      k.seq = p.seq ? (long long)__ldg(p.seq + i) : (p.page_size ? i / p.tok_per_seq : 0);
+      k.pos = p.rotate ? __ldg(p.positions + i) : 0;
+      k.v0 = ap_load8<T, kVec>(x + 8 * lane);
+      k.v1 = ap_load8<T, kVec>(x + 256 + 8 * lane);
+      k.a = x[da];
+      k.b = x[db];
+    }
+    return k;
+  };
+  long long i = (long long)blockIdx.x * kApWarps + (threadIdx.x >> 5);
+  Token cur = load(i);
+  for (; i < p.tokens; i += stride) {
+    const Token k = cur;
+    long long row = k.slot;
+    if (p.page_size && k.slot >= 0) {
       row = -1;
-      if (b >= 0 && b < p.batch && (slot >> 6) < p.pages_per_seq) {
-        const int page = __ldg(p.page_table + b * p.pages_per_seq + (slot >> 6));
-        if (page >= 0) row = (long long)page * 64 + (slot & 63);
+      if (k.seq >= 0 && k.seq < p.batch && (k.slot >> 6) < p.pages_per_seq) {
+        const int page = __ldg(p.page_table + k.seq * p.pages_per_seq + (k.slot >> 6));
+        if (page >= 0) row = (long long)page * 64 + (k.slot & 63);
       }
     }
+    cur = load(i + stride);
+    if (k.slot < 0) continue;                          // no place: nothing is written
     if (row < 0 || row >= p.num_kv_rows) {
       if (lane == 0) atomicOr(&g_error_word, 4u);
       continue;
     }
-    const T* x = static_cast<const T*>(p.x) + i * p.x_stride;
     float v0[8], v1[8];
-    ap_load8<T, kVec>(x + 8 * lane, v0);
-    ap_load8<T, kVec>(x + 256 + 8 * lane, v1);
-    float a = RopeIo<T>::get(x[da]), b = RopeIo<T>::get(x[db]);
+    rope_unpack<T, 8>(k.v0, v0);
+    rope_unpack<T, 8>(k.v1, v1);
+    float a = RopeIo<T>::get(k.a), b = RopeIo<T>::get(k.b);
     if (p.norm_weight) {
       float ss = 0.f;
 #pragma unroll
@@ -112,22 +144,19 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       const float r = rsqrtf(ss * (1.0f / 512.0f) + p.eps);
-      float w0[8], w1[8];
-      ap_load8<float, true>(p.norm_weight + 8 * lane, w0);
-      ap_load8<float, true>(p.norm_weight + 256 + 8 * lane, w1);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v0[j] = v0[j] * r * w0[j];
         v1[j] = v1[j] * r * w1[j];
       }
       if (kDsv4) {
-        a = a * r * __ldg(p.norm_weight + da);
-        b = b * r * __ldg(p.norm_weight + db);
+        a = a * r * wa;
+        b = b * r * wb;
       }
     }
     if (p.rotate) {
       float c, s;
-      rope_sincos(p.table.step[lane], __ldg(p.positions + i), p.table.mscale, c, s);
+      rope_sincos(turn, k.pos, p.table.mscale, c, s);
       const float ra = fmaf(a, c, -b * s);
       b = fmaf(a, s, b * c);
       a = ra;
@@ -148,14 +177,17 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
       // lose bits, so it stops at 2^-126
       const float scale = m > 0.f ? fmaxf(__fdiv_rn(m, 448.0f), 1.1754943508222875e-38f) : 1.0f;
       uint8_t* dst = p.kv + row * kRowBytesFp8;
+      // the quotient by way of the reciprocal: within 2^-23 of x / scale, far
+      // inside the half step of 2^-4 that the codes round by
+      const float inv = __frcp_rn(scale);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v0[j] = __fdiv_rn(v0[j], scale);
-        v1[j] = __fdiv_rn(v1[j], scale);
+        v0[j] *= inv;
+        v1[j] *= inv;
       }
       *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
       *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
-      const uint32_t ab = pack_e4m3x2(__fdiv_rn(a, scale), __fdiv_rn(b, scale));
+      const uint32_t ab = pack_e4m3x2(a * inv, b * inv);
       dst[da] = (uint8_t)ab;
       dst[db] = (uint8_t)(ab >> 8);
       if (lane == 0) p.kv_row_scale[row] = scale;

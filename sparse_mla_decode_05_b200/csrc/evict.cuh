@@ -5,7 +5,6 @@
 namespace smla {
 
 constexpr int kEvThreads = 1024;       // selection: one CTA per sequence
-constexpr int kEvPer = 8;              // keys per thread in registers
 
 static_assert(sizeof(smla_evict_shape) == 48 && offsetof(smla_evict_shape, num_kv_rows) == 32, "smla_evict_shape layout");
 
@@ -24,12 +23,191 @@ __device__ __forceinline__ uint32_t evict_key(float w, int i, int sinks, int tai
   return w == w ? order_key(w) : 0u;
 }
 
-// One CTA per sequence.  Radix select of the budget-th largest key (four
-// digits of eight bits), then the positions above it and the lowest ones
-// equal to it, compacted in ascending order with their weights.  The
-// compaction walks the positions upwards and writes at or below where it
-// reads, so acc_out may be acc.
+// Contexts up to kEvMaxCtas x 16,384 positions: a cluster of CTAs per
+// sequence, every thread holding kPer of its weights in registers, so that
+// the weights are read once and acc_out may be acc.  Radix select of the
+// budget-th largest key by digits of 11, 11 and 10 bits: each CTA counts its
+// keys in shared memory, all read the counts of all (distributed shared
+// memory), and pick the same digit.  Then every key above the selection is
+// kept and the lowest positions equal to it; the CTAs exchange their counts to
+// know where their kept positions go.
+constexpr int kEvMaxCtas = 8;          // the portable cluster size
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void evict_sync(int ctas) {
+  if (ctas > 1) cluster_sync_all();
+  else __syncthreads();
+}
+// Warp 0: exclusive prefix sums, in place, of the 32 kPer counts v[]; returns
+// the total to every lane.
+template <int kPer>
+__device__ __forceinline__ int prefix_counts(int* v) {
+  const int lane = threadIdx.x & 31;
+  int x[kPer], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    x[k] = v[kPer * lane + k];
+    sum += x[k];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  int run = incl - sum;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    v[kPer * lane + k] = run;
+    run += x[k];
+  }
+  return __shfl_sync(0xffffffffu, incl, 31);
+}
+
+template <int kPer>
 __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const SelectParams p) {
+  __shared__ uint32_t hist[2][2048];
+  __shared__ uint32_t total[2048];
+  __shared__ int cnt[32 * kPer];      // [k][warp] counts, then their prefix sums
+  __shared__ int wsum[32];
+  __shared__ int s_total[2];          // this CTA's keys equal to the selection, and its kept keys
+  __shared__ uint32_t s_digit;
+  __shared__ int s_need, s_cnt;
+  grid_dep_wait();
+  const int rank = blockIdx.x, ctas = gridDim.x, b = blockIdx.y;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  int n = p.ctx_len[b];
+  if (n < 0 || n > p.max_ctx) {
+    if (t == 0) atomicOr(&g_error_word, 4u);
+    n = n < 0 ? 0 : p.max_ctx;
+  }
+  const float* acc = p.acc + (size_t)b * p.max_ctx;
+  float* out = p.acc_out + (size_t)b * p.max_ctx;
+  int32_t* kept = p.kept + (size_t)b * p.budget;
+  const int base = rank * kEvThreads * kPer;
+  if (n <= p.budget) {
+    for (int i = rank * kEvThreads + t; i < p.budget; i += ctas * kEvThreads) kept[i] = i < n ? i : -1;
+    if (out != acc)
+      for (int i = rank * kEvThreads + t; i < n; i += ctas * kEvThreads) out[i] = acc[i];
+    // (new_len may be ctx_len: the value the other CTAs then read clamps to the same n)
+    __syncthreads();
+    if (rank == 0 && t == 0) p.new_len[b] = n;
+    return;
+  }
+  const int tail = n - p.recent;
+  float w[kPer];
+  uint32_t key[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = base + k * kEvThreads + t;
+    w[k] = i < n ? acc[i] : 0.f;
+    key[k] = evict_key(w[k], i, p.sinks, tail);
+  }
+  auto valid = [&](int k) -> bool { return base + k * kEvThreads + t < n; };
+  uint32_t prefix = 0, mask = 0;
+  int need = p.budget, eq_count = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+    const uint32_t dmask = pass == 2 ? 1023u : 2047u;
+    uint32_t* h = hist[pass & 1];
+    h[t] = 0;
+    h[t + 1024] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      // keys of one value (weights of zero, protected positions) would queue
+      // at one counter: one atomic for the warp where all its keys agree
+      const bool in = valid(k) && (key[k] & mask) == prefix;
+      const uint32_t digit = (key[k] >> shift) & dmask;
+      const unsigned act = __ballot_sync(0xffffffffu, in);
+      if (!in) continue;
+      const int first = __ffs(act) - 1;
+      const uint32_t d0 = __shfl_sync(act, digit, first);
+      const unsigned same = __ballot_sync(act, digit == d0);
+      if (digit != d0) atomicAdd(&h[digit], 1u);
+      else if (lane == first) atomicAdd(&h[digit], (uint32_t)__popc(same));
+    }
+    evict_sync(ctas);
+    uint32_t c0 = h[t], c1 = h[t + 1024];
+    if (ctas > 1) {
+      c0 = c1 = 0;
+      const uint32_t a = smem_u32(h + t);
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t ra = mapa_shared(a, (uint32_t)r);
+        c0 += ld_cluster_u32(ra);
+        c1 += ld_cluster_u32(ra + 4096);
+      }
+    }
+    total[t] = c0;
+    total[t + 1024] = c1;
+    __syncthreads();
+    radix_pick2048(total, need, wsum, &s_digit, &s_need, &s_cnt);
+    prefix |= s_digit << shift;
+    mask |= dmask << shift;
+    need = s_need;
+    eq_count = s_cnt;
+    __syncthreads();
+  }
+  // Ranks in position order (k, warp, lane), across the cluster's CTAs.
+  const unsigned lt = (1u << lane) - 1u;
+  unsigned selm[kPer];
+  auto ranks = [&](const unsigned (&m)[kPer], int which) -> int {   // cnt: exclusive counts; returns the CTA's offset
+    if (lane == 0) {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) cnt[k * 32 + warp] = __popc(m[k]);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int all = prefix_counts<kPer>(cnt);
+      if (lane == 0) s_total[which] = all;
+    }
+    evict_sync(ctas);
+    int off = 0;
+    const uint32_t a = smem_u32(&s_total[which]);
+    for (int r = 0; r < rank; ++r) off += (int)ld_cluster_u32(mapa_shared(a, (uint32_t)r));
+    return off;
+  };
+  if (eq_count == need) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) selm[k] = __ballot_sync(0xffffffffu, valid(k) && key[k] >= prefix);
+  } else {
+    unsigned eqm[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) eqm[k] = __ballot_sync(0xffffffffu, valid(k) && key[k] == prefix);
+    const int off = ranks(eqm, 0);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int rk = off + cnt[k * 32 + warp] + __popc(eqm[k] & lt);
+      selm[k] = __ballot_sync(0xffffffffu, valid(k) && (key[k] > prefix || (key[k] == prefix && rk < need)));
+    }
+    __syncthreads();   // every rank read before cnt is reused
+  }
+  const int off = ranks(selm, 1);   // (all CTAs have read their weights by here)
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const int i = base + k * kEvThreads + t;
+    if ((selm[k] >> lane) & 1u) {
+      const int pos = off + cnt[k * 32 + warp] + __popc(selm[k] & lt);
+      if (pos < p.budget) {
+        kept[pos] = i;
+        out[pos] = w[k];
+      }
+    }
+    if (i >= p.budget && i < n) out[i] = 0.f;
+  }
+  if (rank == 0 && t == 0) p.new_len[b] = p.budget;
+  if (ctas > 1) cluster_sync_all();   // no CTA leaves while its counts may be read
+}
+
+// Longer contexts: one CTA per sequence re-reads the weights, four digits of
+// eight bits, then a compaction of 1,024 positions at a time that walks
+// upwards and writes at or below where it reads, so acc_out may be acc.
+__global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_long_kernel(const SelectParams p) {
   __shared__ uint32_t hist[256];
   __shared__ int sums[65];
   __shared__ uint32_t s_digit;
@@ -121,56 +299,66 @@ struct CompactParams {
   const int32_t* from;       // page table of the source
   const int32_t* to;         // of the destination (the same: in place)
   int budget, pages_from, pages_to;
+  int log2_slice;            // bytes of a row per CTA (planes of 16-byte units)
+  int chunk;                 // rows per CTA
 };
 
 constexpr int kCpThreads = 256;
-constexpr int kCpSlice = 128;          // bytes of a row per CTA (16-byte units)
 constexpr int kCpBatch = 8;            // rows a thread has in flight
+constexpr int kCpPages = 1024;         // source pages held in shared memory
 
 template <int kUnit> struct UnitOf;
 template <> struct UnitOf<16> { using T = uint4; };
 template <> struct UnitOf<8> { using T = uint2; };
 template <> struct UnitOf<4> { using T = uint32_t; };
 
-// address of a row of a plane, null where the page lies outside the pool
-__device__ __forceinline__ uint8_t* evict_row(const EvictPlane& pl, const int32_t* pages, int npages, int pos) {
-  if ((pos >> 6) >= npages) return nullptr;
-  const int page = __ldg(pages + (pos >> 6));
+// address of row `pos` of a plane through its page, null outside the pool
+__device__ __forceinline__ uint8_t* evict_row(const EvictPlane& pl, int page, int pos) {
   if (page < 0 || (long long)page * 64 + (pos & 63) >= pl.rows_limit) return nullptr;
   return pl.base + page * pl.page_stride + (pos & 63) * (long long)pl.row_stride;
 }
 
-// Moves row kept[i] to row i for every kept position of a sequence, for the
-// byte columns [slice, slice + lanes x unit) of a plane.  In place this is
-// safe without any exchange between CTAs: columns are independent, kept[i] >=
-// i, and a CTA walks i upwards in blocks of R rows, writing a block only after
-// the whole block is read.  Writing rows [i, i + R) destroys only sources
-// that rows up to i + R - 1 needed, all read by then.
+// Moves row kept[i] to row i, i in [lo, hi), for the byte columns [slice, slice
+// + lanes x unit) of a plane.  In place this is safe without any exchange
+// between CTAs: columns are independent, kept[i] >= i, and a CTA walks i
+// upwards in steps, writing a step's rows only after all of them are read.
+// Writing rows [i, i + R) destroys only sources that rows up to i + R - 1
+// needed, all read by then; rows read ahead of a write lie above it.
+// The next step's kept positions are loaded a step ahead and the pages come
+// from shared memory, so that a step waits for one memory latency only.
 template <int kUnit>
-__device__ __forceinline__ void compact_slice(const CompactParams& p, const EvictPlane& pl, int slice, int lanes) {
+__device__ __forceinline__ void compact_slice(const CompactParams& p, const EvictPlane& pl, const int* s_pages, int slice,
+                                              int log2_lanes, int lo, int hi) {
   using U = typename UnitOf<kUnit>::T;
   const int b = blockIdx.y, t = threadIdx.x;
-  const int n = min(p.new_len[b], p.budget);
   const int32_t* kept = p.kept + (size_t)b * p.budget;
   const int32_t* from = p.from + (size_t)b * p.pages_from;
   const int32_t* to = p.to + (size_t)b * p.pages_to;
-  const int rows = kCpThreads / lanes;              // rows per step
-  const int col = slice + (t % lanes) * kUnit, r0 = t / lanes;
-  const bool live = r0 < rows && col < pl.width;
+  const int rows = kCpThreads >> log2_lanes;        // rows per batch element
+  const int col = slice + (t & ((1 << log2_lanes) - 1)) * kUnit, r0 = t >> log2_lanes;
+  const bool live = col < pl.width;
   const bool in_place = p.from == p.to;
   bool outside = false;
-  for (int base = 0; base < n; base += rows * kCpBatch) {
+  int old[kCpBatch];
+#pragma unroll
+  for (int k = 0; k < kCpBatch; ++k) {
+    const int i = lo + k * rows + r0;
+    old[k] = live && i < hi ? __ldg(kept + i) : -1;
+  }
+  for (int base = lo; base < hi; base += rows * kCpBatch) {
     U v[kCpBatch];
     uint8_t* dst[kCpBatch];
 #pragma unroll
     for (int k = 0; k < kCpBatch; ++k) {
-      const int i = base + k * rows + r0;
+      const int i = base + k * rows + r0, o = old[k];
       dst[k] = nullptr;
-      if (!live || i >= n) continue;
-      const int old = __ldg(kept + i);
-      if (old < 0 || (in_place && old == i)) continue;
-      const uint8_t* src = evict_row(pl, from, p.pages_from, old);
-      uint8_t* d = evict_row(pl, to, p.pages_to, i);
+      if (o < 0 || (in_place && o == i)) continue;
+      uint8_t* src = nullptr;
+      if ((o >> 6) < p.pages_from) {
+        const int page = (o >> 6) < kCpPages ? s_pages[o >> 6] : __ldg(from + (o >> 6));
+        src = evict_row(pl, page, o);
+      }
+      uint8_t* d = (i >> 6) < p.pages_to ? evict_row(pl, __ldg(to + (i >> 6)), i) : nullptr;
       if (!src || !d) {
         outside = true;
         continue;
@@ -178,7 +366,12 @@ __device__ __forceinline__ void compact_slice(const CompactParams& p, const Evic
       v[k] = *reinterpret_cast<const U*>(src + col);
       dst[k] = d + col;
     }
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kCpBatch; ++k) {
+      const int i = base + (kCpBatch + k) * rows + r0;
+      old[k] = live && i < hi ? __ldg(kept + i) : -1;
+    }
+    if (in_place) __syncthreads();
 #pragma unroll
     for (int k = 0; k < kCpBatch; ++k)
       if (dst[k]) *reinterpret_cast<U*>(dst[k]) = v[k];
@@ -187,14 +380,22 @@ __device__ __forceinline__ void compact_slice(const CompactParams& p, const Evic
 }
 
 __global__ void __launch_bounds__(kCpThreads) smla_evict_compact_kernel(const __grid_constant__ CompactParams p) {
+  __shared__ int s_pages[kCpPages];
   grid_dep_wait();
+  const int b = blockIdx.y;
+  for (int i = threadIdx.x; i < min(p.pages_from, kCpPages); i += kCpThreads)
+    s_pages[i] = __ldg(p.from + (size_t)b * p.pages_from + i);
+  __syncthreads();
   int k = p.planes - 1;
   while ((int)blockIdx.x < p.plane[k].cta0) --k;
   const EvictPlane& pl = p.plane[k];
-  const int slice = ((int)blockIdx.x - pl.cta0) * kCpSlice;
-  if (pl.unit == 16) compact_slice<16>(p, pl, slice, kCpSlice / 16);
-  else if (pl.unit == 8) compact_slice<8>(p, pl, slice, 1);
-  else compact_slice<4>(p, pl, slice, 1);
+  const int slice = ((int)blockIdx.x - pl.cta0) << p.log2_slice;
+  // (in place: all rows, in order; else chunks of rows)
+  const int n = min(p.new_len[b], p.budget);
+  const int lo = blockIdx.z * p.chunk, hi = min(n, lo + p.chunk);
+  if (pl.unit == 16) compact_slice<16>(p, pl, s_pages, slice, p.log2_slice - 4, lo, hi);
+  else if (pl.unit == 8) compact_slice<8>(p, pl, s_pages, slice, 0, lo, hi);
+  else compact_slice<4>(p, pl, s_pages, slice, 0, lo, hi);
 }
 
 // ------------------------------------------------------------------ host
@@ -225,8 +426,29 @@ static smla_status run_select(const smla_evict_shape* s, const float* acc, const
                               int32_t* new_len, float* acc_out, cudaStream_t stream) {
   SelectParams p = {acc, ctx_len, kept, new_len, acc_out, s->max_ctx, s->budget, s->sinks, s->recent};
   void* args[] = {&p};
-  const cudaError_t e = launch_pdl((const void*)smla_evict_select_kernel, dim3((unsigned)s->batch), dim3(kEvThreads), 0,
-                                   stream, args);
+  cudaError_t e;
+  if (s->max_ctx > kEvMaxCtas * kEvThreads * 16) {
+    e = launch_pdl((const void*)smla_evict_select_long_kernel, dim3((unsigned)s->batch), dim3(kEvThreads), 0, stream, args);
+  } else {
+    // eight weights per thread while the cluster's CTAs hold them all
+    const bool wide = s->max_ctx > kEvMaxCtas * kEvThreads * 8;
+    const int per = kEvThreads * (wide ? 16 : 8);
+    int ctas = 1;
+    while (ctas * per < s->max_ctx) ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)s->batch);
+    cfg.blockDim = dim3(kEvThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)ctas;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    e = cudaLaunchKernelExC(&cfg, wide ? (const void*)smla_evict_select_kernel<16> : (const void*)smla_evict_select_kernel<8>, args);
+  }
   return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
@@ -250,11 +472,20 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
                                void* k_cache, cudaStream_t stream) {
   CompactParams p;
   memset(&p, 0, sizeof(p));
+  const int sms = device_sm_count();
+  if (sms <= 0) return SMLA_ERR_CUDA;
+  const bool in_place = !new_page_table || new_page_table == page_table;
+  // In place a CTA walks all rows of its slice, so few sequences need narrow
+  // slices to spread over the device; new pages are also split by rows.
+  const int row_bytes = s->kv_dtype == SMLA_KV_BF16 ? kRowBytesBf16 : kRowBytesFp8;
+  p.log2_slice = 7;
+  while (in_place && p.log2_slice > 5 && (long long)s->batch * (row_bytes >> p.log2_slice) < sms) --p.log2_slice;
+  p.chunk = in_place ? s->budget : (kCpThreads >> (p.log2_slice - 4)) * kCpBatch;
   int ctas = 0;
   auto plane = [&](void* base, long long page_stride, int row_stride, int width, int unit, long long rows) {
     EvictPlane& pl = p.plane[p.planes++];
     pl = {static_cast<uint8_t*>(base), page_stride, row_stride, width, unit, ctas, (int)rows};
-    ctas += unit == 16 ? (width + kCpSlice - 1) / kCpSlice : 1;
+    ctas += unit == 16 ? (width + (1 << p.log2_slice) - 1) >> p.log2_slice : 1;
   };
   if (s->kv_dtype == SMLA_KV_BF16) {
     plane(kv, 64ll * kRowBytesBf16, kRowBytesBf16, kRowBytesBf16, 16, s->num_kv_rows);
@@ -269,12 +500,13 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
   p.kept = kept;
   p.new_len = new_len;
   p.from = page_table;
-  p.to = new_page_table ? new_page_table : page_table;
+  p.to = in_place ? page_table : new_page_table;
   p.budget = s->budget;
   p.pages_from = s->pages_per_seq;
   p.pages_to = p.to == p.from ? s->pages_per_seq : s->new_pages_per_seq;
   void* args[] = {&p};
-  const cudaError_t e = launch_pdl((const void*)smla_evict_compact_kernel, dim3((unsigned)ctas, (unsigned)s->batch),
+  const cudaError_t e = launch_pdl((const void*)smla_evict_compact_kernel, dim3((unsigned)ctas, (unsigned)s->batch,
+                                                                                   (unsigned)((s->budget + p.chunk - 1) / p.chunk)),
                                    dim3(kCpThreads), 0, stream, args);
   return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }

@@ -62,49 +62,73 @@ struct RopeParams {
   long long xt, xh, yt, yh;     // strides in elements
   int tokens, heads, groups;    // groups: threads per (token, unit) over the heads
   int offset, pairs;            // rotated dims [offset, offset + 2 pairs)
-  int units, rot_units;         // units of a head row: rot_units rotated ones, then the copied ones
+  int rot_units, copy_units;    // units of a head row
   int left;                     // copied units that lie before the rotated dims
   float sign;
   smla_rope_table table;
 };
+
+// kN elements from / to fp32, two at a time where they are 16 bits wide
+template <typename T, int kN>
+__device__ __forceinline__ void rope_unpack(const RopeVec<T, kN>& r, float (&v)[kN]) {
+  if constexpr (sizeof(T) == 2 && kN % 2 == 0) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = RopeIo<T>::get(r.v[i]);
+  }
+}
+template <typename T, int kN>
+__device__ __forceinline__ RopeVec<T, kN> rope_pack(const float (&v)[kN]) {
+  RopeVec<T, kN> r;
+  if constexpr (sizeof(T) == 2 && kN % 2 == 0) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+      else w[i] = pack_f16x2(v[2 * i], v[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) r.v[i] = RopeIo<T>::put(v[i]);
+  }
+  return r;
+}
 
 // Items (token, head group, unit), unit fastest, so that a warp's lanes cover
 // whole head rows.  A thread takes the heads g, g + groups, ... of its item:
 // cos and sin are computed once for them all, and kRopeBatch rows' loads are
 // in flight together.  kN > 1: 16-byte units, of kN / 2 pairs (interleaved)
 // or of kN elements of each half; kN = 1: one pair, element by element.
+// Every thread also passes on its share of the dims outside the rotation, so
+// that the lanes of a warp do the same work.
 template <typename T, int kN, bool kInter>
 __global__ void __launch_bounds__(kRopeThreads) smla_rope_kernel(const __grid_constant__ RopeParams p) {
   using V = RopeVec<T, kN>;
-  using Io = RopeIo<T>;
   constexpr bool kTwo = !kInter || kN == 1;      // the pair's halves are two loads
   constexpr int kPairs = kTwo ? kN : kN / 2;
   grid_dep_wait();
-  const uint32_t per_token = (uint32_t)p.groups * (uint32_t)p.units;
+  const uint32_t per_token = (uint32_t)p.groups * (uint32_t)p.rot_units;
   const unsigned long long item = (unsigned long long)blockIdx.x * kRopeThreads + threadIdx.x;
   // (the host keeps tokens * per_token below 2^32)
   const uint32_t tok = (uint32_t)item / per_token, rest = (uint32_t)item % per_token;
-  const uint32_t g = rest / (uint32_t)p.units, u = rest % (uint32_t)p.units;
+  const int g = (int)(rest / (uint32_t)p.rot_units), u = (int)(rest % (uint32_t)p.rot_units);
   if (item >= (unsigned long long)p.tokens * per_token) return;
   const T* x = static_cast<const T*>(p.x) + (long long)tok * p.xt;
   T* y = static_cast<T*>(p.y) + (long long)tok * p.yt;
-  if ((int)u >= p.rot_units) {
-    // dims outside the rotation, passed on (only when y is not x)
-    const int k = (int)u - p.rot_units;
-    const int d = k < p.left ? k * kN : p.offset + 2 * p.pairs + (k - p.left) * kN;
-    for (int h0 = (int)g; h0 < p.heads; h0 += kRopeBatch * p.groups) {
-      V a[kRopeBatch];
-#pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i)
-        if (h0 + i * p.groups < p.heads) a[i] = *reinterpret_cast<const V*>(x + (long long)(h0 + i * p.groups) * p.xh + d);
-#pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i)
-        if (h0 + i * p.groups < p.heads) *reinterpret_cast<V*>(y + (long long)(h0 + i * p.groups) * p.yh + d) = a[i];
-    }
-    return;
-  }
   const int pos = __ldg(p.positions + tok);
-  const int pair0 = (int)u * kPairs;
+  const int pair0 = u * kPairs;
   float c[kPairs], s[kPairs];
 #pragma unroll
   for (int j = 0; j < kPairs; ++j) {
@@ -112,7 +136,7 @@ __global__ void __launch_bounds__(kRopeThreads) smla_rope_kernel(const __grid_co
     s[j] *= p.sign;
   }
   const int d0 = p.offset + (kInter ? 2 * pair0 : pair0);
-  for (int h0 = (int)g; h0 < p.heads; h0 += kRopeBatch * p.groups) {
+  for (int h0 = g; h0 < p.heads; h0 += kRopeBatch * p.groups) {
     V a[kRopeBatch], b[kRopeBatch];
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
@@ -122,20 +146,34 @@ __global__ void __launch_bounds__(kRopeThreads) smla_rope_kernel(const __grid_co
         if constexpr (kTwo) b[i] = *reinterpret_cast<const V*>(row + (kInter ? 1 : p.pairs));
       }
     }
+    // dims outside the rotation (when y is not x), passed on
+    for (int k = u; k < p.copy_units; k += p.rot_units) {
+      const int d = k < p.left ? k * kN : p.offset + 2 * p.pairs + (k - p.left) * kN;
+      V v[kRopeBatch];
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i)
+        if (h0 + i * p.groups < p.heads) v[i] = *reinterpret_cast<const V*>(x + (long long)(h0 + i * p.groups) * p.xh + d);
+#pragma unroll
+      for (int i = 0; i < kRopeBatch; ++i)
+        if (h0 + i * p.groups < p.heads) *reinterpret_cast<V*>(y + (long long)(h0 + i * p.groups) * p.yh + d) = v[i];
+    }
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i) {
       if (h0 + i * p.groups < p.heads) {
         T* row = y + (long long)(h0 + i * p.groups) * p.yh + d0;
+        float va[kN], vb[kN];
+        rope_unpack<T, kN>(a[i], va);
+        if constexpr (kTwo) rope_unpack<T, kN>(b[i], vb);
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
-          T& ra = kTwo ? a[i].v[j] : a[i].v[(2 * j) % kN];
-          T& rb = kTwo ? b[i].v[j] : a[i].v[(2 * j + 1) % kN];
-          const float u0 = Io::get(ra), u1 = Io::get(rb);
-          ra = Io::put(fmaf(u0, c[j], -u1 * s[j]));
-          rb = Io::put(fmaf(u0, s[j], u1 * c[j]));
+          float& ra = kTwo ? va[j] : va[(2 * j) % kN];
+          float& rb = kTwo ? vb[j] : va[(2 * j + 1) % kN];
+          const float u0 = ra, u1 = rb;
+          ra = fmaf(u0, c[j], -u1 * s[j]);
+          rb = fmaf(u0, s[j], u1 * c[j]);
         }
-        *reinterpret_cast<V*>(row) = a[i];
-        if constexpr (kTwo) *reinterpret_cast<V*>(row + (kInter ? 1 : p.pairs)) = b[i];
+        *reinterpret_cast<V*>(row) = rope_pack<T, kN>(va);
+        if constexpr (kTwo) *reinterpret_cast<V*>(row + (kInter ? 1 : p.pairs)) = rope_pack<T, kN>(vb);
       }
     }
   }
@@ -156,7 +194,7 @@ template <typename T, int kN, bool kInter>
 static cudaError_t launch_rope_as(const RopeParams& prm, long long tokens, cudaStream_t stream) {
   RopeParams p = prm;
   // chunks of tokens whose items stay below 2^31
-  const long long per_token = (long long)p.groups * p.units;
+  const long long per_token = (long long)p.groups * p.rot_units;
   const long long most = ((1ll << 31) - kRopeThreads) / per_token;
   long long left = tokens;
   while (left > 0) {
@@ -188,11 +226,11 @@ static cudaError_t launch_rope(RopeParams p, const smla_rope_shape* s, bool inte
   const int n = vec ? kV : 1;                       // elements per copied unit
   p.rot_units = vec ? (inter ? rot : p.pairs) / kV : p.pairs;
   p.left = before / n;
-  p.units = p.rot_units + p.left + after / n;
-  // Heads per thread: eight share a thread's cos and sin where there is
+  p.copy_units = p.left + after / n;
+  // Heads per thread: up to 16 share a thread's cos and sin where there is
   // enough other work to fill the device, fewer for a few tokens.
-  const long long work = s->tokens * s->heads * p.units;
-  const int per = work >= 148ll * 2048 * 8 ? 8 : (work >= 148ll * 2048 * 2 ? 4 : 1);
+  const long long work = s->tokens * s->heads * p.rot_units, fill = 148ll * 2048;
+  const int per = work >= 8 * 16 * fill ? 16 : (work >= 4 * fill ? 4 : 1);
   p.groups = (s->heads + per - 1) / per;
   if (vec)
     return inter ? launch_rope_as<T, kV, true>(p, s->tokens, stream) : launch_rope_as<T, kV, false>(p, s->tokens, stream);

@@ -56,6 +56,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "sparse_mla.h"
 
