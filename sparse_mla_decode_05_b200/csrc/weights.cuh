@@ -7,11 +7,8 @@
 
 namespace smla {
 
-constexpr int kWtTile = 64;                        // entries per tile (MMA M)
-constexpr int kWtEpiWarps = 8, kWtCopyWarps = 8;
-constexpr int kWtThreads = 32 * (1 + kWtEpiWarps + kWtCopyWarps);
+constexpr int kWtEpiWarps = 8;
 constexpr int kWtRing = 8;                         // tiles whose rows and scales are kept
-constexpr int kWtAtom = kWtTile * 128;             // 128 bytes of each of the 64 rows
 // Shared-memory operands are 128-byte-swizzled atoms of [rows][128 B]; the
 // last 64 bytes of a 576-byte fp8 row are a 64-byte-swizzled atom [rows][64 B].
 template <int kKind>
@@ -19,16 +16,24 @@ struct WtCfg {
   static constexpr bool kFp8 = kKind == kKindFp8;
   static constexpr int kQK = kKind == kKindDsv4 ? 512 : kDqk;
   static constexpr int kRowBytes = kFp8 ? kQK : 2 * kQK;           // of an operand row
-  static constexpr int kStages = kFp8 ? 4 : 2;
-  static constexpr int kStageBytes = kWtTile * kRowBytes;
+  // Entries per tile = MMA M.  The tensor cores take as long for 64 rows as
+  // for 128: fp8 rows, whose bytes arrive fastest per MMA, need the full rate
+  // (64 rows: 47.8 us on the batch of 128, the MMAs busy 63 % of it).
+  static constexpr int kM = kFp8 ? 128 : 64;
+  static constexpr int kAtom = kM * 128;                           // 128 bytes of each of the rows
+  static constexpr int kStages = 2;
+  static constexpr int kStageBytes = kM * kRowBytes;
+  static constexpr int kCopyWarps = kKind == kKindDsv4 ? 16 : 8;
+  static constexpr int kRows = kM / kCopyWarps;                    // rows of a tile per copy warp
+  static constexpr int kThreads = 32 * (1 + kWtEpiWarps + kCopyWarps);
   static constexpr int kQRows = kFp8 ? 128 : 64;                   // fp8: the heads' high parts, then their low parts
   static constexpr int kQBytes = kQRows * kRowBytes;
   static constexpr int kN = kQRows;                                // MMA N: columns of a score buffer
   static constexpr uint32_t kTmem = 2 * kN;
   static constexpr int kSmemQ = kStages * kStageBytes;
-  static constexpr int kSmemRow = kSmemQ + kQBytes;                // int  [kWtRing][64] physical row or -1
-  static constexpr int kSmemScale = kSmemRow + kWtRing * 64 * 4;   // f32  [kWtRing][64] row scale (fp8)
-  static constexpr int kSmemLse = kSmemScale + kWtRing * 64 * 4;   // f32  [2][64] by row parity
+  static constexpr int kSmemRow = kSmemQ + kQBytes;                // int  [kWtRing][kM] physical row or -1
+  static constexpr int kSmemScale = kSmemRow + kWtRing * kM * 4;   // f32  [kWtRing][kM] row scale (fp8)
+  static constexpr int kSmemLse = kSmemScale + kWtRing * kM * 4;   // f32  [2][64] by row parity
   static constexpr int kSmemK = kSmemLse + 2 * 64 * 4;             // f32  [2][64] scale, over the query's power of two
   static constexpr int kSmemBar = kSmemK + 2 * 64 * 4;
   static constexpr int kSmemTmem = kSmemBar + 8 * 16;
@@ -39,7 +44,7 @@ struct WtCfg {
   // the epilogue of tile t to have read its slot.
   static_assert(kWtRing >= kStages + 2, "row ring");
 };
-constexpr uint32_t kIdescWt = make_idesc(64, 64, false, false), kIdescWt8 = make_idesc_e4m3(64, 128, false);
+constexpr uint32_t kIdescWt = make_idesc(64, 64, false, false), kIdescWt8 = make_idesc_e4m3(128, 128, false);
 // barriers
 constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13;
 
@@ -109,74 +114,74 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
     }
     cp_async_wait_all();
   } else {
-    // lane l: chunks l, 32 + l and, of lanes 0-7, 64 + l; four heads at a time
-#pragma unroll 1
-    for (int hh = 0; hh < 8; hh += 4) {
-      uint4 v[4][3];
+    // lane l: chunks l, 32 + l and, of lanes 0-7, 64 + l; four heads' loads in
+    // flight
+    uint4 v[4][3];
+    auto load = [&](int i, int hh) {
+      const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)hh * (C::kQK * 2));
+      v[i][0] = __ldg(src + lane);
+      v[i][1] = __ldg(src + 32 + lane);
+      v[i][2] = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0u, 0u, 0u, 0u);
+    };
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)(hh + i) * (C::kQK * 2));
-        v[i][0] = __ldg(src + lane);
-        v[i][1] = __ldg(src + 32 + lane);
-        v[i][2] = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 4; ++i) load(i, i);
+#pragma unroll
+    for (int hh = 0; hh < 8; ++hh) {
+      const int i = hh & 3, h = h0 + hh;
+      float m = 0.f;
+#pragma unroll
+      for (int u = 0; u < 3; ++u) {
+        const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w4[k] << 16)), fabsf(__uint_as_float(w4[k] & 0xFFFF0000u))));
       }
+      // (the largest of the magnitudes' bits: non-negative floats order as integers)
+      m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));
+      int sq = m > 0.f ? 7 - ilog2f(m) : 0;
+      sq = sq > 120 ? 120 : (sq < -120 ? -120 : sq);
+      const float up = pow2i(sq);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int h = h0 + hh + i;
-        float m = 0.f;
+      for (int u = 0; u < 3; ++u) {
+        if (u == 2 && lane >= 8) continue;
+        const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w4[k] << 16)), fabsf(__uint_as_float(w4[k] & 0xFFFF0000u))));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        // 2^sq as two factors, so that both stay normal for any q
-        int sq = m > 0.f ? 7 - ilog2f(m) : 0;
-        sq = sq > 120 ? 120 : (sq < -120 ? -120 : sq);
-        const float up = pow2i(sq);
-#pragma unroll
-        for (int u = 0; u < 3; ++u) {
-          if (u == 2 && lane >= 8) continue;
-          const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            split_e4m3x2(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xFFFF0000u) * up, hi[k], lo[k]);
-          // eight codes: half of 16-byte chunk (32 u + lane) / 2 of the row
-          const int c = (32 * u + lane) >> 1;
-          const uint32_t at = (uint32_t)(8 * (lane & 1));
-          *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(h, c) + at) =
-              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(64 + h, c) + at) =
-              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-        }
-        if (lane == 0) s_k[h] = p.scale * pow2i(-sq);
+        for (int k = 0; k < 4; ++k)
+          split_e4m3x2(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xFFFF0000u) * up, hi[k], lo[k]);
+        // eight codes: half of 16-byte chunk (32 u + lane) / 2 of the row
+        const int c = (32 * u + lane) >> 1;
+        const uint32_t at = (uint32_t)(8 * (lane & 1));
+        *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(h, c) + at) =
+            make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(64 + h, c) + at) =
+            make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
       }
+      if (lane == 0) s_k[h] = p.scale * pow2i(-sq);
+      if (hh < 4) load(i, hh + 4);
     }
   }
 }
 
-// The decode rows' tiles of 64 entries are laid end to end and shared out
+// The decode rows' tiles are laid end to end and shared out
 // evenly over one CTA per SM; every tile's weights are its own, so nothing is
 // merged.  Warp roles: one MMA issuer; eight epilogue warps, which also
 // stage the query of each row the CTA meets; eight copy warps.
-//  * Copy warp w resolves and gathers rows 8 w .. 8 w + 7 of each tile by
-//    16-byte cp.async (lane = chunk of one row, the rows' last 64 bytes
-//    merged): conflict-free in the swizzled atoms, two to four tiles ahead.
-//  * S[64 entries x 64 heads] = K Q^T in tensor memory, two buffers.  fp8 rows
+//  * Copy warps resolve and gather kRows rows each of every tile by 16-byte
+//    cp.async (lane = chunk of one row, the rows' last 64 bytes merged):
+//    conflict-free in the swizzled atoms, two tiles ahead.
+//  * S[entries x 64 heads] = K Q^T in tensor memory, two buffers.  fp8 rows
 //    are multiplied as stored (kind::f8f6f4) by the query scaled per head by
 //    a power of two and split into e4m3 high and low parts, as in the decode:
 //    columns 0-63 and 64-127 of the buffer.
 //  * Epilogue warps 0-3 take the even tiles, 4-7 the odd ones; a thread has one
-//    entry and 32 heads, the other 32 are its partner's, sixteen lanes on.
+//    entry: of 128-entry tiles all heads, of 64-entry tiles 32, the other 32
+//    being its partner's, sixteen lanes on.
 template <int kKind>
-__global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __grid_constant__ WeightsParams p) {
+__global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel(const __grid_constant__ WeightsParams p) {
   using C = WtCfg<kKind>;
   constexpr bool kFp8 = C::kFp8, kDsv4 = kKind == kKindDsv4;
-  constexpr int kStages = C::kStages;
+  constexpr int kStages = C::kStages, kM = C::kM, kRows = C::kRows, kAtom = C::kAtom;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -194,7 +199,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       // a copying thread's copies (fp8, bf16), and each copy warp's row numbers or converted rows
-      mbar_init(BAR(WB_FULL + i), kWtCopyWarps + (kDsv4 ? 0 : 32 * kWtCopyWarps));
+      mbar_init(BAR(WB_FULL + i), C::kCopyWarps + (kDsv4 ? 0 : 32 * C::kCopyWarps));
       mbar_init(BAR(WB_EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -242,9 +247,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
         const uint64_t da = sw128_desc(a, 16, 1024), db = sw128_desc(b, 16, 1024);
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          mma8_ss_elect(d, da + (uint64_t)((k >> 2) * (kWtAtom >> 4) + (k & 3) * 2),
+          mma8_ss_elect(d, da + (uint64_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2),
                         db + (uint64_t)((k >> 2) * (C::kQRows * 128 >> 4) + (k & 3) * 2), idesc, k > 0);
-        const uint64_t ta = sw64_desc(a + 4 * kWtAtom), tb = sw64_desc(b + 4 * C::kQRows * 128);
+        const uint64_t ta = sw64_desc(a + 4 * kAtom), tb = sw64_desc(b + 4 * C::kQRows * 128);
 #pragma unroll
         for (int k = 0; k < 2; ++k) mma8_ss_elect(d, ta + (uint64_t)(2 * k), tb + (uint64_t)(2 * k), idesc, true);
       } else {
@@ -252,7 +257,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
         const uint64_t da = sw128_desc(a, 16, 1024), db = sw128_desc(b, 16, 1024);
 #pragma unroll
         for (int k = 0; k < C::kQK / 16; ++k) {
-          const uint64_t off = (uint64_t)((k >> 2) * (kWtAtom >> 4) + (k & 3) * 2);
+          const uint64_t off = (uint64_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
           if (k == 0) mma_set_elect(d, da, db, idesc);
           else mma_acc_elect(d, da + off, db + off, idesc);
         }
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
   } else if (warp <= kWtEpiWarps) {
     // -------------------------------------------------------------- epilogue
     const int ew = warp - 1, group = ew >> 2, quarter = warp & 3;
-    const int e = 16 * quarter + (lane & 15), half = lane >> 4;
+    const int e = kM == 128 ? 32 * quarter + lane : 16 * quarter + (lane & 15), half = kM == 128 ? 0 : lane >> 4;
     bool ok = true;
     int row = row0, tin = tin0, seg = 0;
     for (int t = 0; ok && t < count; ++t) {
@@ -275,6 +280,10 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
         if (t > 0) ok = wait_all(WB_SF + ((t - 1) & 1), ((t - 1) >> 1) & 1);
         if (!ok) break;
         const int h0 = 8 * ew, sb = (seg & 1) * 64;
+        // the query of the row after this one, into L2 ahead of its use
+        if (ew == 0 && lane == 0 && t + nt - tin < count)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.q + (size_t)(row + 1) * kH * C::kQK * 2),
+                       "r"(kH * C::kQK * 2) : "memory");
         if (lane < 8) {
           // a head without any valid entry has lse -inf and takes no part
           const float l = __ldg(p.lse + (size_t)row * kH + h0 + lane);
@@ -291,38 +300,54 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
         ok = wait_all(WB_SF + group, (t >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        const int rs = (t % kWtRing) * 64 + e;
+        const int rs = (t % kWtRing) * kM + e;
         const int r = s_row[rs];
         const float rsc = kFp8 ? s_scale[rs] : 1.f;
         const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(group * C::kN);
-        float x[32];
-        tmem_ld_16x32bx2_x32(d, x);
-        if constexpr (kFp8) {
-          float lo[32];
-          tmem_ld_16x32bx2_x32(d + 64, lo);
-          tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 32; ++h) x[h] += lo[h];
-        } else {
-          tmem_wait_ld();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(WB_SE + group));
+        const float* lse = s_lse + ((seg - 1) & 1) * 64 + 32 * half;
+        const float* kh = s_k + ((seg - 1) & 1) * 64 + 32 * half;
         // scale q.k - lse in natural units and one rounding: where a weight is
         // large the difference is small, so the exponential is taken of a
         // number known to its own last bits, not to those of the lse
-        const float* lse = s_lse + ((seg - 1) & 1) * 64 + 32 * half;
-        const float* kh = s_k + ((seg - 1) & 1) * 64 + 32 * half;
-        float sum = 0.f;
+        auto weigh = [&](const float (&x)[32], const float* l, const float* k) -> float {
+          float sum = 0.f;
 #pragma unroll
-        for (int h = 0; h < 32; h += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(lse + h), k4 = *reinterpret_cast<const float4*>(kh + h);
-          sum += ex2(1.44269504f * fmaf(x[h] * rsc, k4.x, -l4.x)) + ex2(1.44269504f * fmaf(x[h + 1] * rsc, k4.y, -l4.y)) +
-                 (ex2(1.44269504f * fmaf(x[h + 2] * rsc, k4.z, -l4.z)) + ex2(1.44269504f * fmaf(x[h + 3] * rsc, k4.w, -l4.w)));
+          for (int h = 0; h < 32; h += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(l + h), k4 = *reinterpret_cast<const float4*>(k + h);
+            sum += ex2(1.44269504f * fmaf(x[h] * rsc, k4.x, -l4.x)) + ex2(1.44269504f * fmaf(x[h + 1] * rsc, k4.y, -l4.y)) +
+                   (ex2(1.44269504f * fmaf(x[h + 2] * rsc, k4.z, -l4.z)) + ex2(1.44269504f * fmaf(x[h + 3] * rsc, k4.w, -l4.w)));
+          }
+          return sum;
+        };
+        float sum = 0.f;
+        if constexpr (kFp8) {
+          // 32 heads at a time: high parts from column 32 hf, low parts from 64 + 32 hf
+          float x[32], lo[32];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            tmem_ld_32x32b_x32(d + 32u * (uint32_t)hf, x);
+            tmem_ld_32x32b_x32(d + 64u + 32u * (uint32_t)hf, lo);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 32; ++h) x[h] += lo[h];
+            if (hf == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(BAR(WB_SE + group));
+            }
+            sum += weigh(x, lse + 32 * hf, kh + 32 * hf);
+          }
+        } else {
+          float x[32];
+          tmem_ld_16x32bx2_x32(d, x);
+          tmem_wait_ld();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(WB_SE + group));
+          sum = weigh(x, lse, kh);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int at = tin * kWtTile + e;
+        const int at = tin * kM + e;
         if (half == 0 && at < p.topk) p.out[(size_t)row * p.topk + at] = r >= 0 ? sum : 0.f;
       }
       if (++tin == nt) {
@@ -332,38 +357,39 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
     }
   } else {
     // ------------------------------------------------------------- copy warps
-    const int cw = warp - 1 - kWtEpiWarps, r8 = lane & 7;
-    // lanes l, l + 8, ... hold row 8 cw + l of a tile: entry of tile t + 2,
-    // row of tile t + 1, and tile t's row being copied
+    const int cw = warp - 1 - kWtEpiWarps, first = kRows * cw;     // rows first .. first + kRows - 1 of a tile
+    // lanes l, l + kRows, ... hold row first + l: entry of tile t + 2, row of
+    // tile t + 1, and tile t's row being copied
     struct Cursor {
       int row, tin;
     };
     Cursor c1{row0, tin0};
     auto next = [&](Cursor c) -> Cursor { return c.tin + 1 == nt ? Cursor{c.row + 1, 0} : Cursor{c.row, c.tin + 1}; };
     auto entry = [&](Cursor c, int t) -> int {
-      const int at = c.tin * kWtTile + 8 * cw + r8;
+      const int at = c.tin * kM + first + (lane & (kRows - 1));
       return t < count && at < p.topk ? __ldg(p.indices + (size_t)c.row * p.topk + at) : -1;
     };
     int r0 = resolve_row(p, entry(c1, 0), row0);
     c1 = next(c1);
     int i1 = entry(c1, 1);
     for (int t = 0; t < count; ++t) {
-      const int stage = t % kStages, rs = (t % kWtRing) * 64;
+      const int stage = t % kStages, rs = (t % kWtRing) * kM;
       const int r1 = resolve_row(p, i1, c1.row);
       c1 = next(c1);
       i1 = entry(c1, t + 2);
       const uint32_t base = sbase + (uint32_t)(stage * C::kStageBytes);
       if constexpr (kDsv4) {
         // codes to bf16 on the way: the loads first, then the stage's turn
-        uint4 v[9];
-        uint2 dsc[9];
+        constexpr int kU = (36 * kRows + 31) / 32;
+        uint4 v[kU];
+        uint2 dsc[kU];
 #pragma unroll
-        for (int u = 0; u < 9; ++u) {
+        for (int u = 0; u < kU; ++u) {
           const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr;      // chunk j of the warp's row rr
           const int r = __shfl_sync(0xffffffffu, r0, rr);
           v[u] = make_uint4(0u, 0u, 0u, 0u);
           dsc[u] = make_uint2(0u, 0u);
-          if (r >= 0) {
+          if (r >= 0 && rr < kRows) {
             const uint8_t* page = p.kv + (size_t)(r >> 6) * kDsv4Page;
             v[u] = __ldg(reinterpret_cast<const uint4*>(page + (r & 63) * kDsv4Slot + 16 * j));
             dsc[u] = __ldg(reinterpret_cast<const uint2*>(page + kDsv4ScaleOff + (r & 63) * 8));
@@ -371,10 +397,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
         }
         if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
 #pragma unroll
-        for (int u = 0; u < 9; ++u) {
-          const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr, tok = 8 * cw + rr;
+        for (int u = 0; u < kU; ++u) {
+          const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr, tok = first + rr;
+          if (rr >= kRows) continue;
           if (j >= 28) {
-            st_shared_v4(base + 7 * kWtAtom + sw128_off(tok, j - 28), v[u]);
+            st_shared_v4(base + 7 * kAtom + sw128_off(tok, j - 28), v[u]);
           } else {
             const int g = j >> 2;
             const uint32_t s2 = ue8m0_bf16x2(((g < 4 ? dsc[u].x : dsc[u].y) >> (8 * (g & 3))) & 0xFFu);
@@ -383,46 +410,49 @@ __global__ void __launch_bounds__(kWtThreads, 1) smla_weights_kernel(const __gri
             e4m3x4_to_bf16x4_scaled(v[u].y, s2, lo.z, lo.w);
             e4m3x4_to_bf16x4_scaled(v[u].z, s2, hi.x, hi.y);
             e4m3x4_to_bf16x4_scaled(v[u].w, s2, hi.z, hi.w);
-            st_shared_v4(base + g * kWtAtom + sw128_off(tok, 2 * (j & 3)), lo);
-            st_shared_v4(base + g * kWtAtom + sw128_off(tok, 2 * (j & 3) + 1), hi);
+            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (j & 3)), lo);
+            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (j & 3) + 1), hi);
           }
         }
-        if (lane < 8) s_row[rs + 8 * cw + lane] = r0;
+        if (lane < kRows) s_row[rs + first + lane] = r0;
         fence_proxy_async_smem();
       } else {
         if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
-        // one instruction per row and 512 bytes, then the eight rows' tails
+        // one instruction per row and 512 bytes, then the rows' tails
         // together.  Absent rows read nothing and are zero.
 #pragma unroll
-        for (int rr = 0; rr < 8; ++rr) {
+        for (int rr = 0; rr < kRows; ++rr) {
           const int r = __shfl_sync(0xffffffffu, r0, rr);
           const uint32_t n = r >= 0 ? 16u : 0u;
           const uint8_t* src = p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + lane * 16;
           if constexpr (kFp8) {
-            cp_async_16(base + wt_off8<kWtTile>(8 * cw + rr, lane), src, n);
+            cp_async_16(base + wt_off8<kM>(first + rr, lane), src, n);
           } else {
-            const uint32_t at = base + (uint32_t)((lane >> 3) * kWtAtom) + sw128_off(8 * cw + rr, lane & 7);
+            const uint32_t at = base + (uint32_t)((lane >> 3) * kAtom) + sw128_off(first + rr, lane & 7);
             cp_async_16(at, src, n);
-            cp_async_16(at + 4 * kWtAtom, src + 512, n);
+            cp_async_16(at + 4 * kAtom, src + 512, n);
           }
         }
         if constexpr (kFp8) {
-          const int rr = lane >> 2, r = __shfl_sync(0xffffffffu, r0, rr);
-          cp_async_16(base + wt_off8<kWtTile>(8 * cw + rr, 32 + (lane & 3)),
-                      p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 512 + (lane & 3) * 16, r >= 0 ? 16u : 0u);
+#pragma unroll
+          for (int hh = 0; hh < kRows / 8; ++hh) {
+            const int rr = 8 * hh + (lane >> 2), r = __shfl_sync(0xffffffffu, r0, rr);
+            cp_async_16(base + wt_off8<kM>(first + rr, 32 + (lane & 3)),
+                        p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 512 + (lane & 3) * 16, r >= 0 ? 16u : 0u);
+          }
           // the row's scale rides along (a copy of four bytes)
-          if (lane < 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_scale + rs + 8 * cw + lane)),
+          if (lane < kRows)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_scale + rs + first + lane)),
                          "l"(p.kv_row_scale + (r0 >= 0 ? r0 : 0)) : "memory");
         } else {
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
+          for (int hh = 0; hh < kRows / 4; ++hh) {
             const int rr = 4 * hh + (lane >> 3), r = __shfl_sync(0xffffffffu, r0, rr);
-            cp_async_16(base + 8 * kWtAtom + sw128_off(8 * cw + rr, lane & 7),
+            cp_async_16(base + 8 * kAtom + sw128_off(first + rr, lane & 7),
                         p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 1024 + (lane & 7) * 16, r >= 0 ? 16u : 0u);
           }
         }
-        if (lane < 8) s_row[rs + 8 * cw + lane] = r0;
+        if (lane < kRows) s_row[rs + first + lane] = r0;
         cp_async_mbar_arrive_noinc(BAR(WB_FULL + stage));
       }
       __syncwarp();
@@ -521,7 +551,7 @@ static cudaError_t launch_weights(WeightsParams& p, cudaStream_t stream) {
   if (sms <= 0) return cudaErrorInvalidDevice;
   void* args[] = {&p};
   return launch_pdl((const void*)smla_weights_kernel<kKind>, dim3((unsigned)(p.total < sms ? p.total : sms)),
-                    dim3(kWtThreads), bytes, stream, args);
+                    dim3(WtCfg<kKind>::kThreads), bytes, stream, args);
 }
 
 static smla_status run_weights(const smla_shape* s, const void* q, const void* kv, const float* kv_row_scale,
@@ -550,7 +580,8 @@ static smla_status run_weights(const smla_shape* s, const void* q, const void* k
   p.page_size = s->page_size;
   p.pages_per_seq = s->pages_per_seq;
   p.num_kv_rows = (int)s->num_kv_rows;
-  p.ntiles = (s->topk + kWtTile - 1) / kWtTile;
+  const int m = fp8 ? WtCfg<kKindFp8>::kM : (s->kv_dtype == SMLA_KV_DSV4_PAGED ? WtCfg<kKindDsv4>::kM : WtCfg<kKindBf16>::kM);
+  p.ntiles = (s->topk + m - 1) / m;
   p.total = (long long)rows_of(s) * p.ntiles;
   p.scale = scale;
   const cudaError_t e = fp8 ? launch_weights<kKindFp8>(p, stream)
