@@ -14,6 +14,7 @@
 namespace smla {
 
 constexpr int kApWarps = 4;            // warps per CTA, one token per warp at a time
+constexpr int kApCtas = 6;             // CTAs per SM (85 registers a thread)
 
 static_assert(sizeof(smla_append_shape) == 56 && offsetof(smla_append_shape, x_dtype) == 24, "smla_append_shape layout");
 
@@ -72,7 +73,7 @@ __device__ __forceinline__ uint32_t ap_ue8m0(float amax) {
 // its own: for DeepSeek-V4 pages those are dims 448 - 511, which lanes 24 -
 // 31 hold too for the mean square).  A group of 64 dims is eight lanes.
 template <typename T, int kKind, bool kVec>
-__global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr bool kDsv4 = kKind == kKindDsv4;
   constexpr int kR = kDsv4 ? 448 : 512;                // first rotated dim
   grid_dep_wait();
@@ -97,8 +98,7 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
   struct Token {
     RopeVec<T, 8> v0, v1;
     T a, b;
-    int slot, pos;
-    long long seq;
+    int slot, pos, seq;
   };
   auto load = [&](long long i) -> Token {
     Token k;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
     if (i < p.tokens) {
       const T* x = static_cast<const T*>(p.x) + i * p.x_stride;
       k.slot = __ldg(p.slots + i);
-      k.seq = p.seq ? (long long)__ldg(p.seq + i) : (p.page_size ? i / p.tok_per_seq : 0);
+      k.seq = p.seq ? __ldg(p.seq + i) : (p.page_size ? (int)((uint32_t)i / (uint32_t)p.tok_per_seq) : 0);
       k.pos = p.rotate ? __ldg(p.positions + i) : 0;
       k.v0 = ap_load8<T, kVec>(x + 8 * lane);
       k.v1 = ap_load8<T, kVec>(x + 256 + 8 * lane);
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
     if (p.page_size && k.slot >= 0) {
       row = -1;
       if (k.seq >= 0 && k.seq < p.batch && (k.slot >> 6) < p.pages_per_seq) {
-        const int page = __ldg(p.page_table + k.seq * p.pages_per_seq + (k.slot >> 6));
+        const int page = __ldg(p.page_table + (long long)k.seq * p.pages_per_seq + (k.slot >> 6));
         if (page >= 0) row = (long long)page * 64 + (k.slot & 63);
       }
     }
@@ -136,18 +136,20 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
     float v0[8], v1[8];
     rope_unpack<T, 8>(k.v0, v0);
     rope_unpack<T, 8>(k.v1, v1);
-    float a = RopeIo<T>::get(k.a), b = RopeIo<T>::get(k.b);
+    float a = RopeIo<T>::get(k.a), b = RopeIo<T>::get(k.b), r = 1.f;
     if (p.norm_weight) {
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = fmaf(v0[j], v0[j], fmaf(v1[j], v1[j], ss));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = rsqrtf(ss * (1.0f / 512.0f) + p.eps);
+      // (1 / rms goes to the row's largest value and to the final scaling of
+      // fp8 rows, not to every element on the way)
+      r = rsqrtf(ss * (1.0f / 512.0f) + p.eps);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v0[j] = v0[j] * r * w0[j];
-        v1[j] = v1[j] * r * w1[j];
+        v0[j] *= w0[j];
+        v1[j] *= w1[j];
       }
       if (kDsv4) {
         a = a * r * wa;
@@ -163,6 +165,11 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
     }
     if constexpr (kKind == kKindBf16) {
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.kv) + row * kDqk;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v0[j] *= r;
+        v1[j] *= r;
+      }
       *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
                                                              pack_bf16x2(v0[4], v0[5]), pack_bf16x2(v0[6], v0[7]));
       *reinterpret_cast<uint4*>(dst + 256 + 8 * lane) = make_uint4(
@@ -170,20 +177,20 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
       dst[da] = __float2bfloat16_rn(a);
       dst[db] = __float2bfloat16_rn(b);
     } else if constexpr (kKind == kKindFp8) {
-      float m = fmaxf(fmaxf(ap_amax8(v0), ap_amax8(v1)), fmaxf(fabsf(a), fabsf(b)));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float m = fmaxf(fmaxf(ap_amax8(v0), ap_amax8(v1)) * r, fmaxf(fabsf(a), fabsf(b)));
+      // (magnitudes order as their bits do)
+      m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));
       // a row of zeros keeps scale 1; a scale below the normal range would
       // lose bits, so it stops at 2^-126
       const float scale = m > 0.f ? fmaxf(__fdiv_rn(m, 448.0f), 1.1754943508222875e-38f) : 1.0f;
       uint8_t* dst = p.kv + row * kRowBytesFp8;
-      // the quotient by way of the reciprocal: within 2^-23 of x / scale, far
+      // the quotient by way of the reciprocal: within 2^-22 of x / scale, far
       // inside the half step of 2^-4 that the codes round by
-      const float inv = __frcp_rn(scale);
+      const float inv = __frcp_rn(scale), rinv = r * inv;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v0[j] *= inv;
-        v1[j] *= inv;
+        v0[j] *= rinv;
+        v1[j] *= rinv;
       }
       *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
       *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
@@ -193,20 +200,19 @@ __global__ void __launch_bounds__(kApWarps * 32) smla_append_kernel(const __grid
       if (lane == 0) p.kv_row_scale[row] = scale;
     } else {
       // groups 0-3 are lanes 8 g .. 8 g + 7 of v0, groups 4-6 those of v1
-      float m0 = ap_amax8(v0), m1 = ap_amax8(v1);
+      float m0 = ap_amax8(v0) * r, m1 = ap_amax8(v1) * r;
 #pragma unroll
       for (int o = 4; o > 0; o >>= 1) {
         m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
         m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
       }
       const uint32_t e0 = ap_ue8m0(m0), e1 = ap_ue8m0(m1);
-      // division by 2^(e - 127): exact, as a product with 2^(127 - e) in two
-      // factors that are both normal
-      auto down = [](float (&v)[8], uint32_t e) {
-        const int k = 127 - (int)e, k0 = k / 2;
-        const float f0 = pow2i(k0), f1 = pow2i(k - k0);
+      // 2^(127 - e) is a normal number for e <= 253 and halves once more for
+      // 254; the product with it is exact
+      auto down = [&](float (&v)[8], uint32_t e) {
+        const float f = (e < 254 ? pow2i(127 - (int)e) : 0.5f * pow2i(-126)) * 1.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = v[j] * f0 * f1;
+        for (int j = 0; j < 8; ++j) v[j] = v[j] * r * f;
       };
       down(v0, e0);
       down(v1, e1);
@@ -233,8 +239,8 @@ template <typename T, int kKind>
 static cudaError_t launch_append(AppendParams& p, bool vec, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // resident warps: 16 CTAs of four warps per SM; more tokens loop
-  const long long ctas = (p.tokens + kApWarps - 1) / kApWarps, most = 16ll * sms;
+  // as many CTAs as are resident at once; more tokens loop
+  const long long ctas = (p.tokens + kApWarps - 1) / kApWarps, most = (long long)kApCtas * sms;
   void* args[] = {&p};
   const void* kern = vec ? (const void*)smla_append_kernel<T, kKind, true> : (const void*)smla_append_kernel<T, kKind, false>;
   return launch_pdl(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kApWarps * 32), 0, stream, args);

@@ -289,7 +289,7 @@ struct EvictPlane {
   int row_stride, width;     // bytes from row to row in a page; bytes moved per row
   int unit;                  // bytes per thread and row: 16, 8 or 4
   int cta0;                  // first CTA (blockIdx.x) of the plane
-  int rows_limit;            // rows in the plane
+  int pages;                 // pages in the plane
 };
 struct CompactParams {
   EvictPlane plane[3];
@@ -305,18 +305,12 @@ struct CompactParams {
 
 constexpr int kCpThreads = 256;
 constexpr int kCpBatch = 8;            // rows a thread has in flight
-constexpr int kCpPages = 1024;         // source pages held in shared memory
+constexpr int kCpPages = 512;          // pages of a sequence held in shared memory (the rest read as needed)
 
 template <int kUnit> struct UnitOf;
 template <> struct UnitOf<16> { using T = uint4; };
 template <> struct UnitOf<8> { using T = uint2; };
 template <> struct UnitOf<4> { using T = uint32_t; };
-
-// address of row `pos` of a plane through its page, null outside the pool
-__device__ __forceinline__ uint8_t* evict_row(const EvictPlane& pl, int page, int pos) {
-  if (page < 0 || (long long)page * 64 + (pos & 63) >= pl.rows_limit) return nullptr;
-  return pl.base + page * pl.page_stride + (pos & 63) * (long long)pl.row_stride;
-}
 
 // Moves row kept[i] to row i, i in [lo, hi), for the byte columns [slice, slice
 // + lanes x unit) of a plane.  In place this is safe without any exchange
@@ -324,78 +318,84 @@ __device__ __forceinline__ uint8_t* evict_row(const EvictPlane& pl, int page, in
 // upwards in steps, writing a step's rows only after all of them are read.
 // Writing rows [i, i + R) destroys only sources that rows up to i + R - 1
 // needed, all read by then; rows read ahead of a write lie above it.
-// The next step's kept positions are loaded a step ahead and the pages come
-// from shared memory, so that a step waits for one memory latency only.
+// Each step's physical rows are worked out once, by one thread per row and a
+// step ahead (kept position -> page -> row, both page tables in shared
+// memory), so the moving threads wait for one memory latency a step and
+// spend few instructions on addresses.
 template <int kUnit>
-__device__ __forceinline__ void compact_slice(const CompactParams& p, const EvictPlane& pl, const int* s_pages, int slice,
-                                              int log2_lanes, int lo, int hi) {
+__device__ __forceinline__ void compact_slice(const CompactParams& p, const EvictPlane& pl, const int* s_from, const int* s_to,
+                                              int2 (*s_rows)[kCpThreads * kCpBatch], int slice, int log2_lanes, int lo, int hi) {
   using U = typename UnitOf<kUnit>::T;
   const int b = blockIdx.y, t = threadIdx.x;
   const int32_t* kept = p.kept + (size_t)b * p.budget;
-  const int32_t* from = p.from + (size_t)b * p.pages_from;
-  const int32_t* to = p.to + (size_t)b * p.pages_to;
   const int rows = kCpThreads >> log2_lanes;        // rows per batch element
+  const int step = rows * kCpBatch;                 // rows per step (at most kCpThreads x kCpBatch)
   const int col = slice + (t & ((1 << log2_lanes) - 1)) * kUnit, r0 = t >> log2_lanes;
   const bool live = col < pl.width;
   const bool in_place = p.from == p.to;
   bool outside = false;
-  int old[kCpBatch];
-#pragma unroll
-  for (int k = 0; k < kCpBatch; ++k) {
-    const int i = lo + k * rows + r0;
-    old[k] = live && i < hi ? __ldg(kept + i) : -1;
-  }
-  for (int base = lo; base < hi; base += rows * kCpBatch) {
+  // (source, destination) of the rows of the step at `base`; -1: nothing moves
+  auto prepare = [&](int base, int2* to_rows) {
+    for (int j = t; j < step; j += kCpThreads) {
+      const int i = base + j;
+      int2 r = make_int2(-1, -1);
+      if (i < hi) {
+        const int o = __ldg(kept + i);
+        if (o >= 0 && !(in_place && o == i)) {
+          const int ps = o >> 6, pd = i >> 6;
+          const int fp = ps < p.pages_from ? (ps < kCpPages ? s_from[ps] : __ldg(p.from + (size_t)b * p.pages_from + ps)) : -1;
+          const int tp = pd < p.pages_to ? (pd < kCpPages ? s_to[pd] : __ldg(p.to + (size_t)b * p.pages_to + pd)) : -1;
+          if (fp >= 0 && tp >= 0 && fp < pl.pages && tp < pl.pages) r = make_int2(fp * 64 + (o & 63), tp * 64 + (i & 63));
+          else outside = true;
+        }
+      }
+      to_rows[j] = r;
+    }
+  };
+  prepare(lo, s_rows[0]);
+  int buf = 0;
+  for (int base = lo; base < hi; base += step, buf ^= 1) {
+    __syncthreads();
     U v[kCpBatch];
-    uint8_t* dst[kCpBatch];
+    int to[kCpBatch];
 #pragma unroll
     for (int k = 0; k < kCpBatch; ++k) {
-      const int i = base + k * rows + r0, o = old[k];
-      dst[k] = nullptr;
-      if (o < 0 || (in_place && o == i)) continue;
-      uint8_t* src = nullptr;
-      if ((o >> 6) < p.pages_from) {
-        const int page = (o >> 6) < kCpPages ? s_pages[o >> 6] : __ldg(from + (o >> 6));
-        src = evict_row(pl, page, o);
-      }
-      uint8_t* d = (i >> 6) < p.pages_to ? evict_row(pl, __ldg(to + (i >> 6)), i) : nullptr;
-      if (!src || !d) {
-        outside = true;
-        continue;
-      }
-      v[k] = *reinterpret_cast<const U*>(src + col);
-      dst[k] = d + col;
+      const int2 r = s_rows[buf][k * rows + r0];
+      to[k] = live ? r.y : -1;
+      if (to[k] >= 0)
+        v[k] = *reinterpret_cast<const U*>(pl.base + (r.x >> 6) * pl.page_stride + (uint32_t)((r.x & 63) * pl.row_stride + col));
     }
-#pragma unroll
-    for (int k = 0; k < kCpBatch; ++k) {
-      const int i = base + (kCpBatch + k) * rows + r0;
-      old[k] = live && i < hi ? __ldg(kept + i) : -1;
-    }
+    if (base + step < hi) prepare(base + step, s_rows[buf ^ 1]);
     if (in_place) __syncthreads();
 #pragma unroll
     for (int k = 0; k < kCpBatch; ++k)
-      if (dst[k]) *reinterpret_cast<U*>(dst[k]) = v[k];
+      if (to[k] >= 0)
+        *reinterpret_cast<U*>(pl.base + (to[k] >> 6) * pl.page_stride + (uint32_t)((to[k] & 63) * pl.row_stride + col)) = v[k];
   }
   if (outside) atomicOr(&g_error_word, 4u);
 }
 
 __global__ void __launch_bounds__(kCpThreads) smla_evict_compact_kernel(const __grid_constant__ CompactParams p) {
-  __shared__ int s_pages[kCpPages];
+  __shared__ int s_from[kCpPages], s_to[kCpPages];
+  __shared__ int2 s_rows[2][kCpThreads * kCpBatch];
   grid_dep_wait();
   const int b = blockIdx.y;
-  for (int i = threadIdx.x; i < min(p.pages_from, kCpPages); i += kCpThreads)
-    s_pages[i] = __ldg(p.from + (size_t)b * p.pages_from + i);
+  // (in place: all rows, in order; else chunks of rows)
+  const int n = min(p.new_len[b], p.budget);
+  const int lo = blockIdx.z * p.chunk, hi = min(n, lo + p.chunk);
+  if (lo >= hi) return;
+  for (int i = threadIdx.x; i < kCpPages; i += kCpThreads) {
+    if (i < p.pages_from) s_from[i] = __ldg(p.from + (size_t)b * p.pages_from + i);
+    if (i < p.pages_to) s_to[i] = __ldg(p.to + (size_t)b * p.pages_to + i);
+  }
   __syncthreads();
   int k = p.planes - 1;
   while ((int)blockIdx.x < p.plane[k].cta0) --k;
   const EvictPlane& pl = p.plane[k];
   const int slice = ((int)blockIdx.x - pl.cta0) << p.log2_slice;
-  // (in place: all rows, in order; else chunks of rows)
-  const int n = min(p.new_len[b], p.budget);
-  const int lo = blockIdx.z * p.chunk, hi = min(n, lo + p.chunk);
-  if (pl.unit == 16) compact_slice<16>(p, pl, s_pages, slice, p.log2_slice - 4, lo, hi);
-  else if (pl.unit == 8) compact_slice<8>(p, pl, s_pages, slice, 0, lo, hi);
-  else compact_slice<4>(p, pl, s_pages, slice, 0, lo, hi);
+  if (pl.unit == 16) compact_slice<16>(p, pl, s_from, s_to, s_rows, slice, p.log2_slice - 4, lo, hi);
+  else if (pl.unit == 8) compact_slice<8>(p, pl, s_from, s_to, s_rows, slice, 0, lo, hi);
+  else compact_slice<4>(p, pl, s_from, s_to, s_rows, slice, 0, lo, hi);
 }
 
 // ------------------------------------------------------------------ host
@@ -484,7 +484,7 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
   int ctas = 0;
   auto plane = [&](void* base, long long page_stride, int row_stride, int width, int unit, long long rows) {
     EvictPlane& pl = p.plane[p.planes++];
-    pl = {static_cast<uint8_t*>(base), page_stride, row_stride, width, unit, ctas, (int)rows};
+    pl = {static_cast<uint8_t*>(base), page_stride, row_stride, width, unit, ctas, (int)(rows / 64)};
     ctas += unit == 16 ? (width + (1 << p.log2_slice) - 1) >> p.log2_slice : 1;
   };
   if (s->kv_dtype == SMLA_KV_BF16) {
