@@ -14,7 +14,8 @@
 namespace smla {
 
 constexpr int kApWarps = 4;            // warps per CTA, one token per warp at a time
-constexpr int kApCtas = 6;             // CTAs per SM (85 registers a thread)
+constexpr int kApCtas = 6;             // CTAs per SM (80 registers a thread)
+constexpr int kApStages = 3;           // rows of its run that a warp has under way
 
 static_assert(sizeof(smla_append_shape) == 56 && offsetof(smla_append_shape, x_dtype) == 24, "smla_append_shape layout");
 
@@ -31,6 +32,7 @@ struct AppendParams {
   int page_size, pages_per_seq, batch, tok_per_seq;
   float eps;
   int rotate;
+  int run;                        // consecutive tokens per warp, at most 32
   smla_rope_table table;
 };
 
@@ -69,18 +71,71 @@ __device__ __forceinline__ uint32_t ap_ue8m0(float amax) {
 }
 
 // One warp per token.  Lane l holds dims 8 l .. 8 l + 7 and 256 + 8 l .. +7
-// of the 512 normalised dims, and pair l of the 64 rotated ones (loaded on
+// of the 512 normalised dims, and pair l of the 64 rotated ones (read on
 // its own: for DeepSeek-V4 pages those are dims 448 - 511, which lanes 24 -
 // 31 hold too for the mean square).  A group of 64 dims is eight lanes.
+//
+// A warp takes a run of up to 32 consecutive tokens: their places are worked
+// out once, a token per lane, and the rows come by bulk copies into a ring of
+// kApStages rows of the warp's own, so that a token's arithmetic waits neither
+// for its row nor for its place and holds no registers for rows to come.
+// (Rows that are not 16-byte aligned are loaded as they are needed.)
 template <typename T, int kKind, bool kVec>
 __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr bool kDsv4 = kKind == kKindDsv4;
   constexpr int kR = kDsv4 ? 448 : 512;                // first rotated dim
+  constexpr int kWidth = kDsv4 ? kDv : kDqk;
+  constexpr int kRowB = kWidth * (int)sizeof(T);
+  __shared__ __align__(16) uint8_t s_x[kVec ? kApWarps * kApStages * kRowB : 16];
+  __shared__ __align__(8) unsigned long long s_bar[kApWarps * kApStages];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t bar = smem_u32(s_bar + warp * kApStages);
+  if (kVec) {
+    if (lane == 0) {
+      for (int k = 0; k < kApStages; ++k) mbar_init(bar + 8u * (uint32_t)k, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+  }
   grid_dep_wait();
-  const int lane = threadIdx.x & 31;
+  const long long first = ((long long)blockIdx.x * kApWarps + warp) * p.run;
+  const int count = (int)min((long long)p.run, p.tokens - first);
+  if (count <= 0) return;
+  const T* xs = static_cast<const T*>(p.x) + first * p.x_stride;
+  auto fetch = [&](int j) {
+    const int st = j % kApStages;
+    mbar_arrive_expect_tx(bar + 8u * (uint32_t)st, kRowB);
+    bulk_load_g2s(smem_u32(s_x) + (uint32_t)((warp * kApStages + st) * kRowB), xs + j * p.x_stride, kRowB,
+                  bar + 8u * (uint32_t)st);
+  };
+  if (kVec && lane == 0)
+    for (int j = 0; j < min(count, kApStages); ++j) fetch(j);
+  // lane j: the place of the run's token j and its position.  Slots are
+  // physical rows, or positions through the page table of the token's
+  // sequence, as the decode's index entries are.  A place: the row, or -1
+  // (skipped, or out of range and reported)
+  int place = -1, position = 0;
+  if (lane < count) {
+    const long long i = first + lane;
+    const int slot = __ldg(p.slots + i);
+    if (p.rotate) position = __ldg(p.positions + i);
+    long long row = slot;
+    if (p.page_size && slot >= 0) {
+      const int seq = p.seq ? __ldg(p.seq + i) : (int)((uint32_t)i / (uint32_t)p.tok_per_seq);
+      row = -2;
+      if (seq >= 0 && seq < p.batch && (slot >> 6) < p.pages_per_seq) {
+        const int page = __ldg(p.page_table + (long long)seq * p.pages_per_seq + (slot >> 6));
+        if (page >= 0) row = (long long)page * 64 + (slot & 63);
+      }
+    }
+    if (slot >= 0 && (row < 0 || row >= p.num_kv_rows)) {
+      atomicOr(&g_error_word, 4u);
+      row = -1;
+    }
+    place = row >= 0 ? (int)row : -1;
+  }
   const bool inter = p.table.layout == SMLA_ROPE_INTERLEAVED;
   const int da = kR + (inter ? 2 * lane : lane), db = inter ? da + 1 : da + 32;
-  const long long stride = (long long)gridDim.x * kApWarps;
   const unsigned long long turn = p.table.step[lane];
   float w0[8], w1[8], wa = 1.f, wb = 1.f;
   if (p.norm_weight) {
@@ -91,52 +146,26 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       wb = __ldg(p.norm_weight + db);
     }
   }
-  // The next token's loads are issued before this one's arithmetic.  The row
-  // itself does not wait for its place: slots are physical rows, or
-  // positions through the page table of the token's sequence, as the decode's
-  // index entries are.
-  struct Token {
-    RopeVec<T, 8> v0, v1;
-    T a, b;
-    int slot, pos, seq;
-  };
-  auto load = [&](long long i) -> Token {
-    Token k;
-    k.slot = -1;
-    if (i < p.tokens) {
-      const T* x = static_cast<const T*>(p.x) + i * p.x_stride;
-      k.slot = __ldg(p.slots + i);
-      k.seq = p.seq ? __ldg(p.seq + i) : (p.page_size ? (int)((uint32_t)i / (uint32_t)p.tok_per_seq) : 0);
-      k.pos = p.rotate ? __ldg(p.positions + i) : 0;
-      k.v0 = ap_load8<T, kVec>(x + 8 * lane);
-      k.v1 = ap_load8<T, kVec>(x + 256 + 8 * lane);
-      k.a = x[da];
-      k.b = x[db];
+  for (int j = 0; j < count; ++j) {
+    const long long row = __shfl_sync(0xffffffffu, place, j);
+    const int pos = __shfl_sync(0xffffffffu, position, j);
+    const T* x = xs + j * p.x_stride;
+    if constexpr (kVec) {
+      const int st = j % kApStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(bar + 8u * (uint32_t)st, (uint32_t)((j / kApStages) & 1)))) return;
+      x = reinterpret_cast<const T*>(s_x + (warp * kApStages + st) * kRowB);
     }
-    return k;
-  };
-  long long i = (long long)blockIdx.x * kApWarps + (threadIdx.x >> 5);
-  Token cur = load(i);
-  for (; i < p.tokens; i += stride) {
-    const Token k = cur;
-    long long row = k.slot;
-    if (p.page_size && k.slot >= 0) {
-      row = -1;
-      if (k.seq >= 0 && k.seq < p.batch && (k.slot >> 6) < p.pages_per_seq) {
-        const int page = __ldg(p.page_table + (long long)k.seq * p.pages_per_seq + (k.slot >> 6));
-        if (page >= 0) row = (long long)page * 64 + (k.slot & 63);
-      }
+    const RopeVec<T, 8> x0 = ap_load8<T, kVec>(x + 8 * lane), x1 = ap_load8<T, kVec>(x + 256 + 8 * lane);
+    const T xa = x[da], xb = x[db];
+    if (kVec) {
+      __syncwarp();                                    // the ring's row has been read by all lanes
+      if (lane == 0 && j + kApStages < count) fetch(j + kApStages);
     }
-    cur = load(i + stride);
-    if (k.slot < 0) continue;                          // no place: nothing is written
-    if (row < 0 || row >= p.num_kv_rows) {
-      if (lane == 0) atomicOr(&g_error_word, 4u);
-      continue;
-    }
+    if (row < 0) continue;                             // no place: nothing is written
     float v0[8], v1[8];
-    rope_unpack<T, 8>(k.v0, v0);
-    rope_unpack<T, 8>(k.v1, v1);
-    float a = RopeIo<T>::get(k.a), b = RopeIo<T>::get(k.b), r = 1.f;
+    rope_unpack<T, 8>(x0, v0);
+    rope_unpack<T, 8>(x1, v1);
+    float a = RopeIo<T>::get(xa), b = RopeIo<T>::get(xb), r = 1.f;
     if (p.norm_weight) {
       float ss = 0.f;
 #pragma unroll
@@ -158,7 +187,7 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
     }
     if (p.rotate) {
       float c, s;
-      rope_sincos(turn, k.pos, p.table.mscale, c, s);
+      rope_sincos(turn, pos, p.table.mscale, c, s);
       const float ra = fmaf(a, c, -b * s);
       b = fmaf(a, s, b * c);
       a = ra;
@@ -174,8 +203,12 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
                                                              pack_bf16x2(v0[4], v0[5]), pack_bf16x2(v0[6], v0[7]));
       *reinterpret_cast<uint4*>(dst + 256 + 8 * lane) = make_uint4(
           pack_bf16x2(v1[0], v1[1]), pack_bf16x2(v1[2], v1[3]), pack_bf16x2(v1[4], v1[5]), pack_bf16x2(v1[6], v1[7]));
-      dst[da] = __float2bfloat16_rn(a);
-      dst[db] = __float2bfloat16_rn(b);
+      if (inter) {
+        *reinterpret_cast<uint32_t*>(dst + da) = pack_bf16x2(a, b);
+      } else {
+        dst[da] = __float2bfloat16_rn(a);
+        dst[db] = __float2bfloat16_rn(b);
+      }
     } else if constexpr (kKind == kKindFp8) {
       float m = fmaxf(fmaxf(ap_amax8(v0), ap_amax8(v1)) * r, fmaxf(fabsf(a), fabsf(b)));
       // (magnitudes order as their bits do)
@@ -195,8 +228,12 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
       *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
       const uint32_t ab = pack_e4m3x2(a * inv, b * inv);
-      dst[da] = (uint8_t)ab;
-      dst[db] = (uint8_t)(ab >> 8);
+      if (inter) {
+        *reinterpret_cast<uint16_t*>(dst + da) = (uint16_t)ab;
+      } else {
+        dst[da] = (uint8_t)ab;
+        dst[db] = (uint8_t)(ab >> 8);
+      }
       if (lane == 0) p.kv_row_scale[row] = scale;
     } else {
       // groups 0-3 are lanes 8 g .. 8 g + 7 of v0, groups 4-6 those of v1
@@ -210,7 +247,7 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       // 2^(127 - e) is a normal number for e <= 253 and halves once more for
       // 254; the product with it is exact
       auto down = [&](float (&v)[8], uint32_t e) {
-        const float f = (e < 254 ? pow2i(127 - (int)e) : 0.5f * pow2i(-126)) * 1.0f;
+        const float f = e < 254 ? pow2i(127 - (int)e) : 0.5f * pow2i(-126);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] * r * f;
       };
@@ -221,8 +258,12 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
       if (lane < 24) *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
       __nv_bfloat16* rope = reinterpret_cast<__nv_bfloat16*>(dst + kDsv4Nope);
-      rope[da - kR] = __float2bfloat16_rn(a);
-      rope[db - kR] = __float2bfloat16_rn(b);
+      if (inter) {
+        *reinterpret_cast<uint32_t*>(rope + da - kR) = pack_bf16x2(a, b);
+      } else {
+        rope[da - kR] = __float2bfloat16_rn(a);
+        rope[db - kR] = __float2bfloat16_rn(b);
+      }
       uint2 block = make_uint2(0u, 0u);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -239,11 +280,14 @@ template <typename T, int kKind>
 static cudaError_t launch_append(AppendParams& p, bool vec, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // as many CTAs as are resident at once; more tokens loop
-  const long long ctas = (p.tokens + kApWarps - 1) / kApWarps, most = (long long)kApCtas * sms;
+  // runs as long as fill the resident warps once, at most 32 tokens
+  const long long resident = (long long)kApCtas * kApWarps * sms;
+  p.run = (int)((p.tokens + resident - 1) / resident);
+  if (p.run > 32) p.run = 32;
+  const long long per_cta = (long long)kApWarps * p.run;
   void* args[] = {&p};
   const void* kern = vec ? (const void*)smla_append_kernel<T, kKind, true> : (const void*)smla_append_kernel<T, kKind, false>;
-  return launch_pdl(kern, dim3((unsigned)(ctas < most ? ctas : most)), dim3(kApWarps * 32), 0, stream, args);
+  return launch_pdl(kern, dim3((unsigned)((p.tokens + per_cta - 1) / per_cta)), dim3(kApWarps * 32), 0, stream, args);
 }
 template <typename T>
 static cudaError_t launch_append_kind(AppendParams& p, int kv_dtype, bool vec, cudaStream_t stream) {
