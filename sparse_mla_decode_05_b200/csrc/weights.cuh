@@ -25,7 +25,13 @@ struct WtCfg {
   static constexpr int kStageBytes = kM * kRowBytes;
   static constexpr int kCopyWarps = kKind == kKindDsv4 ? 16 : 8;
   static constexpr int kRows = kM / kCopyWarps;                    // rows of a tile per copy warp
-  static constexpr int kThreads = 32 * (1 + kWtEpiWarps + kCopyWarps);
+  // fp8: eight warps more help the epilogue warps to stage the query.  Staged by
+  // eight, a row's query took 10,000 cycles, longer than two stages of copies
+  // last; by the copy warps too, it held up the copies.
+  static constexpr int kHelpers = kFp8 ? 8 : 0;
+  static constexpr int kThreads = 32 * (1 + kWtEpiWarps + kCopyWarps + kHelpers);
+  static constexpr int kQWarps = kWtEpiWarps + kHelpers;           // that stage the query
+  static constexpr int kQHeads = kH / kQWarps;
   static constexpr int kQRows = kFp8 ? 128 : 64;                   // fp8: the heads' high parts, then their low parts
   static constexpr int kQBytes = kQRows * kRowBytes;
   static constexpr int kN = kQRows;                                // MMA N: columns of a score buffer
@@ -46,7 +52,7 @@ struct WtCfg {
 };
 constexpr uint32_t kIdescWt = make_idesc(64, 64, false, false), kIdescWt8 = make_idesc_e4m3(128, 128, false);
 // barriers
-constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13;
+constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13, WB_ROW = 14;
 
 // Shared-memory matrix descriptor, 64-byte swizzle (layout type 4), K-major:
 // rows of 64 B, 8-row groups 512 B apart.
@@ -95,12 +101,38 @@ __device__ __forceinline__ int resolve_row(const P& p, int idx, int drow) {
   return (int)r;
 }
 
-// Eight heads of a row's query (h0 .. h0 + 7) into the B operand, by one warp.
+// 32 lanes x 16 columns: thread t reads columns [c, c+16) of lane base+t.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// x (f16x2, |x| < 448) = hi + lo in e4m3x2: hi = e4m3(x), lo = e4m3(x - hi)
+__device__ __forceinline__ void split_e4m3x2_f16(uint32_t x, uint32_t& hi, uint32_t& lo) {
+  uint16_t h, l;
+  uint32_t h16, r16;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r16) : "r"(x), "r"(h16));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r16));
+  hi = h;
+  lo = l;
+}
+
+// kHeads heads of a row's query (h0 ..) into the B operand, by one warp.
 // bf16 caches: as they are.  fp8: times the power of two that brings the
 // head's largest |q| into [128, 256), split into e4m3 high and low parts
 // (exact for the bf16 values whose parts are e4m3 normals, within 2^-10 of the
-// scaled value otherwise); s_k[h] receives scale over that power.
-template <int kKind>
+// scaled value otherwise); s_k[h] receives scale over that power.  This runs
+// once per row between two rows' products, at a warp's own pace (a few cycles
+// an instruction), so it is spread over as many warps as there are and kept
+// short: bf16 pairs are scaled as pairs and split as f16 pairs.
+template <int kKind, int kHeads>
 __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* smem, uint32_t sbase, int row, int h0,
                                                int lane, float* s_k) {
   using C = WtCfg<kKind>;
@@ -108,47 +140,47 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
   const uint8_t* q = p.q + ((size_t)row * kH + h0) * (C::kQK * 2);
   const uint32_t qb = sbase + C::kSmemQ;
   if constexpr (!C::kFp8) {
-    for (int c = lane; c < 8 * kChunks; c += 32) {
+    for (int c = lane; c < kHeads * kChunks; c += 32) {
       const int h = c / kChunks, j = c - h * kChunks;
       cp_async_16(qb + (uint32_t)((j >> 3) * (C::kQRows * 128)) + sw128_off(h0 + h, j & 7), q + (size_t)c * 16, 16u);
     }
     cp_async_wait_all();
   } else {
-    // lane l: chunks l, 32 + l and, of lanes 0-7, 64 + l; four heads' loads in
-    // flight
-    uint4 v[4][3];
-    auto load = [&](int i, int hh) {
-      const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)hh * (C::kQK * 2));
+    // lane l: chunks l, 32 + l and, of lanes 0-7, 64 + l
+    uint4 v[kHeads][3];
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)i * (C::kQK * 2));
       v[i][0] = __ldg(src + lane);
       v[i][1] = __ldg(src + 32 + lane);
       v[i][2] = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0u, 0u, 0u, 0u);
-    };
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) load(i, i);
-#pragma unroll
-    for (int hh = 0; hh < 8; ++hh) {
-      const int i = hh & 3, h = h0 + hh;
-      float m = 0.f;
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = h0 + i;
+      // largest magnitude (bf16 bits order as the magnitudes do)
+      uint32_t m2 = 0;
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
-        const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          m = fmaxf(m, fmaxf(fabsf(__uint_as_float(w4[k] << 16)), fabsf(__uint_as_float(w4[k] & 0xFFFF0000u))));
+        m2 = __vmaxu2(m2, v[i][u].x & 0x7FFF7FFFu);
+        m2 = __vmaxu2(m2, v[i][u].y & 0x7FFF7FFFu);
+        m2 = __vmaxu2(m2, v[i][u].z & 0x7FFF7FFFu);
+        m2 = __vmaxu2(m2, v[i][u].w & 0x7FFF7FFFu);
       }
-      // (the largest of the magnitudes' bits: non-negative floats order as integers)
-      m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));
-      int sq = m > 0.f ? 7 - ilog2f(m) : 0;
+      const uint32_t m = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+      int sq = m ? 134 - (int)(m >> 7) : 0;          // 7 - floor(log2 m)
       sq = sq > 120 ? 120 : (sq < -120 ? -120 : sq);
-      const float up = pow2i(sq);
+      const uint32_t up = (uint32_t)(127 + sq) * 0x00800080u;       // 2^sq as a bf16 pair
 #pragma unroll
       for (int u = 0; u < 3; ++u) {
         if (u == 2 && lane >= 8) continue;
         const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          split_e4m3x2(__uint_as_float(w4[k] << 16) * up, __uint_as_float(w4[k] & 0xFFFF0000u) * up, hi[k], lo[k]);
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t y = bf16x2_mul(w4[k], up);
+          split_e4m3x2_f16(pack_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)), hi[k], lo[k]);
+        }
         // eight codes: half of 16-byte chunk (32 u + lane) / 2 of the row
         const int c = (32 * u + lane) >> 1;
         const uint32_t at = (uint32_t)(8 * (lane & 1));
@@ -158,7 +190,6 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
             make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
       }
       if (lane == 0) s_k[h] = p.scale * pow2i(-sq);
-      if (hh < 4) load(i, hh + 4);
     }
   }
 }
@@ -166,7 +197,8 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
 // The decode rows' tiles are laid end to end and shared out
 // evenly over one CTA per SM; every tile's weights are its own, so nothing is
 // merged.  Warp roles: one MMA issuer; eight epilogue warps, which also
-// stage the query of each row the CTA meets; eight copy warps.
+// stage the query of each row the CTA meets (for fp8 rows with eight more);
+// the copy warps.
 //  * Copy warps resolve and gather kRows rows each of every tile by 16-byte
 //    cp.async (lane = chunk of one row, the rows' last 64 bytes merged):
 //    conflict-free in the swizzled atoms, two tiles ahead.
@@ -206,8 +238,9 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
       mbar_init(BAR(WB_SF + i), 1);
       mbar_init(BAR(WB_SE + i), kWtEpiWarps / 2);
     }
-    mbar_init(BAR(WB_Q), kWtEpiWarps);
+    mbar_init(BAR(WB_Q), C::kQWarps);
     mbar_init(BAR(WB_FIN), 1);
+    mbar_init(BAR(WB_ROW), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -264,6 +297,7 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
       }
       commit_elect(BAR(WB_EMPTY + stage));
       commit_elect(BAR(WB_SF + buf));
+      if (tin + 1 == nt) commit_elect(BAR(WB_ROW));    // the row's last products: its query may go
     }
     // every MMA issued has completed before teardown
     commit_elect(BAR(WB_FIN));
@@ -277,7 +311,7 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
     for (int t = 0; ok && t < count; ++t) {
       if (t == 0 || tin == 0) {
         // the row's query, once the last row's products are done
-        if (t > 0) ok = wait_all(WB_SF + ((t - 1) & 1), ((t - 1) >> 1) & 1);
+        if (t > 0) ok = wait_all(WB_ROW, (seg - 1) & 1);
         if (!ok) break;
         const int h0 = 8 * ew, sb = (seg & 1) * 64;
         // the query of the row after this one, into L2 ahead of its use
@@ -290,7 +324,7 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
           s_lse[sb + h0 + lane] = l == -INFINITY ? INFINITY : l;
           if (!kFp8) s_k[sb + h0 + lane] = p.scale;
         }
-        wt_stage_query<kKind>(p, smem, sbase, row, h0, lane, s_k + sb);
+        wt_stage_query<kKind, C::kQHeads>(p, smem, sbase, row, C::kQHeads * ew, lane, s_k + sb);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(WB_Q));
@@ -309,42 +343,41 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
         // scale q.k - lse in natural units and one rounding: where a weight is
         // large the difference is small, so the exponential is taken of a
         // number known to its own last bits, not to those of the lse
-        auto weigh = [&](const float (&x)[32], const float* l, const float* k) -> float {
+        auto weigh = [&](const float* x, const float* l, const float* k) -> float {   // 16 heads
           float sum = 0.f;
 #pragma unroll
-          for (int h = 0; h < 32; h += 4) {
+          for (int h = 0; h < 16; h += 4) {
             const float4 l4 = *reinterpret_cast<const float4*>(l + h), k4 = *reinterpret_cast<const float4*>(k + h);
             sum += ex2(1.44269504f * fmaf(x[h] * rsc, k4.x, -l4.x)) + ex2(1.44269504f * fmaf(x[h + 1] * rsc, k4.y, -l4.y)) +
                    (ex2(1.44269504f * fmaf(x[h + 2] * rsc, k4.z, -l4.z)) + ex2(1.44269504f * fmaf(x[h + 3] * rsc, k4.w, -l4.w)));
           }
           return sum;
         };
+        auto taken = [&]() {      // the score buffer has been read
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(BAR(WB_SE + group));
+        };
         float sum = 0.f;
         if constexpr (kFp8) {
-          // 32 heads at a time: high parts from column 32 hf, low parts from 64 + 32 hf
-          float x[32], lo[32];
+          // 16 heads at a time: high parts from column 16 g, low parts from 64 + 16 g
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            tmem_ld_32x32b_x32(d + 32u * (uint32_t)hf, x);
-            tmem_ld_32x32b_x32(d + 64u + 32u * (uint32_t)hf, lo);
+          for (int g = 0; g < 4; ++g) {
+            float x[16], lo[16];
+            tmem_ld_32x32b_x16(d + 16u * (uint32_t)g, x);
+            tmem_ld_32x32b_x16(d + 64u + 16u * (uint32_t)g, lo);
             tmem_wait_ld();
+            if (g == 3) taken();
 #pragma unroll
-            for (int h = 0; h < 32; ++h) x[h] += lo[h];
-            if (hf == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(BAR(WB_SE + group));
-            }
-            sum += weigh(x, lse + 32 * hf, kh + 32 * hf);
+            for (int h = 0; h < 16; ++h) x[h] += lo[h];
+            sum += weigh(x, lse + 16 * g, kh + 16 * g);
           }
         } else {
           float x[32];
           tmem_ld_16x32bx2_x32(d, x);
           tmem_wait_ld();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(WB_SE + group));
-          sum = weigh(x, lse, kh);
+          taken();
+          sum = weigh(x, lse, kh) + weigh(x + 16, lse + 16, kh + 16);
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         }
         const int at = tin * kM + e;
@@ -354,6 +387,17 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
         tin = 0;
         ++row;
       }
+    }
+  } else if (C::kHelpers > 0 && warp > kWtEpiWarps + C::kCopyWarps) {
+    // ---------------------------------------------------------- query helpers
+    const int hw = warp - 1 - C::kCopyWarps;          // 8 .. 15: their place among the staging warps
+    int row = row0, tin = tin0, seg = 0;
+    for (int t = 0; t < count; t += nt - tin, tin = 0, ++row, ++seg) {
+      if (t > 0 && !wait_all(WB_ROW, (seg - 1) & 1)) break;
+      wt_stage_query<kKind, C::kQHeads>(p, smem, sbase, row, C::kQHeads * hw, lane, s_k + (seg & 1) * 64);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(WB_Q));
     }
   } else {
     // ------------------------------------------------------------- copy warps
