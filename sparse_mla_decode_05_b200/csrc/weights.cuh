@@ -413,6 +413,23 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
       const int at = c.tin * kM + first + (lane & (kRows - 1));
       return t < count && at < p.topk ? __ldg(p.indices + (size_t)c.row * p.topk + at) : -1;
     };
+    // DeepSeek-V4: a tile's part in registers.  Lane l has chunk l (16 codes, or
+    // from chunk 28 on eight bf16 dims) of each of the warp's rows and the scale
+    // of its 64 dims; lanes 0 - 15 also one of the rows' last four chunks.
+    uint4 va[kRows + 1], vb[kRows + 1];
+    uint32_t sa[kRows], sb[kRows];
+    auto dsv4_load = [&](int rows, uint4 (&v)[kRows + 1], uint32_t (&sc)[kRows]) {
+#pragma unroll
+      for (int u = 0; u <= kRows; ++u) {
+        const int r = __shfl_sync(0xffffffffu, rows, u < kRows ? u : (lane >> 2) & (kRows - 1));
+        v[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (u < kRows) sc[u] = 127u;
+        if (r < 0 || (u == kRows && lane >= 4 * kRows)) continue;
+        const uint8_t* page = p.kv + (size_t)(r >> 6) * kDsv4Page;
+        v[u] = __ldg(reinterpret_cast<const uint4*>(page + (r & 63) * kDsv4Slot + 16 * (u < kRows ? lane : 32 + (lane & 3))));
+        if (u < kRows && lane < 28) sc[u] = __ldg(page + kDsv4ScaleOff + (r & 63) * 8 + (lane >> 2));
+      }
+    };
     int r0 = resolve_row(p, entry(c1, 0), row0);
     c1 = next(c1);
     int i1 = entry(c1, 1);
@@ -423,41 +440,31 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
       i1 = entry(c1, t + 2);
       const uint32_t base = sbase + (uint32_t)(stage * C::kStageBytes);
       if constexpr (kDsv4) {
-        // codes to bf16 on the way: the loads first, then the stage's turn
-        constexpr int kU = (36 * kRows + 31) / 32;
-        uint4 v[kU];
-        uint2 dsc[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr;      // chunk j of the warp's row rr
-          const int r = __shfl_sync(0xffffffffu, r0, rr);
-          v[u] = make_uint4(0u, 0u, 0u, 0u);
-          dsc[u] = make_uint2(0u, 0u);
-          if (r >= 0 && rr < kRows) {
-            const uint8_t* page = p.kv + (size_t)(r >> 6) * kDsv4Page;
-            v[u] = __ldg(reinterpret_cast<const uint4*>(page + (r & 63) * kDsv4Slot + 16 * j));
-            dsc[u] = __ldg(reinterpret_cast<const uint2*>(page + kDsv4ScaleOff + (r & 63) * 8));
-          }
-        }
+        // codes to bf16 on the way, a tile's loads ahead of the stores
+        if (t == 0) dsv4_load(r0, va, sa);
+        dsv4_load(r1, vb, sb);
         if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
+        const int g = lane >> 2;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const int c = 32 * u + lane, rr = c / 36, j = c - 36 * rr, tok = first + rr;
-          if (rr >= kRows) continue;
-          if (j >= 28) {
-            st_shared_v4(base + 7 * kAtom + sw128_off(tok, j - 28), v[u]);
-          } else {
-            const int g = j >> 2;
-            const uint32_t s2 = ue8m0_bf16x2(((g < 4 ? dsc[u].x : dsc[u].y) >> (8 * (g & 3))) & 0xFFu);
+        for (int u = 0; u < kRows; ++u) {
+          const int tok = first + u;
+          if (lane < 28) {
+            const uint32_t s2 = ue8m0_bf16x2(sa[u]);
             uint4 lo, hi;
-            e4m3x4_to_bf16x4_scaled(v[u].x, s2, lo.x, lo.y);
-            e4m3x4_to_bf16x4_scaled(v[u].y, s2, lo.z, lo.w);
-            e4m3x4_to_bf16x4_scaled(v[u].z, s2, hi.x, hi.y);
-            e4m3x4_to_bf16x4_scaled(v[u].w, s2, hi.z, hi.w);
-            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (j & 3)), lo);
-            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (j & 3) + 1), hi);
+            e4m3x4_to_bf16x4_scaled(va[u].x, s2, lo.x, lo.y);
+            e4m3x4_to_bf16x4_scaled(va[u].y, s2, lo.z, lo.w);
+            e4m3x4_to_bf16x4_scaled(va[u].z, s2, hi.x, hi.y);
+            e4m3x4_to_bf16x4_scaled(va[u].w, s2, hi.z, hi.w);
+            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (lane & 3)), lo);
+            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (lane & 3) + 1), hi);
+          } else {
+            st_shared_v4(base + 7 * kAtom + sw128_off(tok, lane - 28), va[u]);
           }
         }
+        if (lane < 4 * kRows) st_shared_v4(base + 7 * kAtom + sw128_off(first + g, 4 + (lane & 3)), va[kRows]);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) va[u] = vb[u], sa[u] = sb[u];
+        va[kRows] = vb[kRows];
         if (lane < kRows) s_row[rs + first + lane] = r0;
         fence_proxy_async_smem();
       } else {
