@@ -402,12 +402,13 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
   } else {
     // ------------------------------------------------------------- copy warps
     const int cw = warp - 1 - kWtEpiWarps, first = kRows * cw;     // rows first .. first + kRows - 1 of a tile
-    // lanes l, l + kRows, ... hold row first + l: entry of tile t + 2, row of
-    // tile t + 1, and tile t's row being copied
+    // lanes l, l + kRows, ... hold row first + l: the entry of tile t + 3, its
+    // rows of tiles t + 2 and t + 1, and tile t's row being copied, so that
+    // neither the entry nor its page is waited for
     struct Cursor {
       int row, tin;
     };
-    Cursor c1{row0, tin0};
+    Cursor c2{row0, tin0};
     auto next = [&](Cursor c) -> Cursor { return c.tin + 1 == nt ? Cursor{c.row + 1, 0} : Cursor{c.row, c.tin + 1}; };
     auto entry = [&](Cursor c, int t) -> int {
       const int at = c.tin * kM + first + (lane & (kRows - 1));
@@ -430,45 +431,48 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
         if (u < kRows && lane < 28) sc[u] = __ldg(page + kDsv4ScaleOff + (r & 63) * 8 + (lane >> 2));
       }
     };
-    int r0 = resolve_row(p, entry(c1, 0), row0);
-    c1 = next(c1);
-    int i1 = entry(c1, 1);
-    for (int t = 0; t < count; ++t) {
+    const int i0 = entry(c2, 0);
+    c2 = next(c2);
+    const int i1 = entry(c2, 1);
+    int r0 = resolve_row(p, i0, row0), r1 = resolve_row(p, i1, c2.row);
+    c2 = next(c2);
+    int i2 = entry(c2, 2);
+    // one tile: true unless a wait gave up.  (DeepSeek-V4: stores `now`, loads the
+    // next tile's part into `then`; the two swap from tile to tile, as moving
+    // registers would wait for the loads.)
+    auto copy_tile = [&](int t, uint4 (&now)[kRows + 1], uint32_t (&snow)[kRows], uint4 (&then)[kRows + 1],
+                         uint32_t (&sthen)[kRows]) -> bool {
       const int stage = t % kStages, rs = (t % kWtRing) * kM;
-      const int r1 = resolve_row(p, i1, c1.row);
-      c1 = next(c1);
-      i1 = entry(c1, t + 2);
+      const int r2 = resolve_row(p, i2, c2.row);
+      c2 = next(c2);
+      i2 = entry(c2, t + 3);
       const uint32_t base = sbase + (uint32_t)(stage * C::kStageBytes);
       if constexpr (kDsv4) {
-        // codes to bf16 on the way, a tile's loads ahead of the stores
-        if (t == 0) dsv4_load(r0, va, sa);
-        dsv4_load(r1, vb, sb);
-        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
+        // codes to bf16 on the way
+        dsv4_load(r1, then, sthen);
+        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) return false;
         const int g = lane >> 2;
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
           const int tok = first + u;
           if (lane < 28) {
-            const uint32_t s2 = ue8m0_bf16x2(sa[u]);
+            const uint32_t s2 = ue8m0_bf16x2(snow[u]);
             uint4 lo, hi;
-            e4m3x4_to_bf16x4_scaled(va[u].x, s2, lo.x, lo.y);
-            e4m3x4_to_bf16x4_scaled(va[u].y, s2, lo.z, lo.w);
-            e4m3x4_to_bf16x4_scaled(va[u].z, s2, hi.x, hi.y);
-            e4m3x4_to_bf16x4_scaled(va[u].w, s2, hi.z, hi.w);
+            e4m3x4_to_bf16x4_scaled(now[u].x, s2, lo.x, lo.y);
+            e4m3x4_to_bf16x4_scaled(now[u].y, s2, lo.z, lo.w);
+            e4m3x4_to_bf16x4_scaled(now[u].z, s2, hi.x, hi.y);
+            e4m3x4_to_bf16x4_scaled(now[u].w, s2, hi.z, hi.w);
             st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (lane & 3)), lo);
             st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (lane & 3) + 1), hi);
           } else {
-            st_shared_v4(base + 7 * kAtom + sw128_off(tok, lane - 28), va[u]);
+            st_shared_v4(base + 7 * kAtom + sw128_off(tok, lane - 28), now[u]);
           }
         }
-        if (lane < 4 * kRows) st_shared_v4(base + 7 * kAtom + sw128_off(first + g, 4 + (lane & 3)), va[kRows]);
-#pragma unroll
-        for (int u = 0; u < kRows; ++u) va[u] = vb[u], sa[u] = sb[u];
-        va[kRows] = vb[kRows];
+        if (lane < 4 * kRows) st_shared_v4(base + 7 * kAtom + sw128_off(first + g, 4 + (lane & 3)), now[kRows]);
         if (lane < kRows) s_row[rs + first + lane] = r0;
         fence_proxy_async_smem();
       } else {
-        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
+        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) return false;
         // one instruction per row and 512 bytes, then the rows' tails
         // together.  Absent rows read nothing and are zero.
 #pragma unroll
@@ -509,6 +513,16 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(WB_FULL + stage));
       r0 = r1;
+      r1 = r2;
+      return true;
+    };
+    if constexpr (kDsv4) {
+      dsv4_load(r0, va, sa);
+      for (int t = 0; t < count; t += 2)
+        if (!copy_tile(t, va, sa, vb, sb) || (t + 1 < count && !copy_tile(t + 1, vb, sb, va, sa))) break;
+    } else {
+      for (int t = 0; t < count; ++t)
+        if (!copy_tile(t, va, sa, vb, sb)) break;
     }
     cp_async_wait_all();
   }
