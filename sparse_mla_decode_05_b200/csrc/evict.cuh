@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
   __shared__ uint32_t s_digit;
   __shared__ int s_need, s_cnt;
   grid_dep_wait();
+  grid_dep_launch();
   const int rank = blockIdx.x, ctas = gridDim.x, b = blockIdx.y;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   int n = p.ctx_len[b];
@@ -133,25 +134,33 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
       else if (lane == first) atomicAdd(&h[digit], (uint32_t)__popc(same));
     }
     evict_sync(ctas);
-    uint32_t c0 = h[t], c1 = h[t + 1024];
     if (ctas > 1) {
-      c0 = c1 = 0;
+      // (all loads on their way before the first is used)
+      uint32_t x[kEvMaxCtas], y[kEvMaxCtas];
       const uint32_t a = smem_u32(h + t);
-      for (int r = 0; r < ctas; ++r) {
-        const uint32_t ra = mapa_shared(a, (uint32_t)r);
-        c0 += ld_cluster_u32(ra);
-        c1 += ld_cluster_u32(ra + 4096);
+#pragma unroll
+      for (int r = 0; r < kEvMaxCtas; ++r) {
+        x[r] = y[r] = 0;
+        if (r < ctas) {
+          const uint32_t ra = mapa_shared(a, (uint32_t)r);
+          x[r] = ld_cluster_u32(ra);
+          y[r] = ld_cluster_u32(ra + 4096);
+        }
       }
+      uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+      for (int r = 0; r < kEvMaxCtas; ++r) c0 += x[r], c1 += y[r];
+      total[t] = c0;
+      total[t + 1024] = c1;
+      __syncthreads();
     }
-    total[t] = c0;
-    total[t + 1024] = c1;
-    __syncthreads();
-    radix_pick2048(total, need, wsum, &s_digit, &s_need, &s_cnt);
+    radix_pick2048(ctas > 1 ? total : h, need, wsum, &s_digit, &s_need, &s_cnt);
     prefix |= s_digit << shift;
     mask |= dmask << shift;
     need = s_need;
     eq_count = s_cnt;
     __syncthreads();
+    if (eq_count == need) break;      // every key that starts with these digits is kept (the same in all CTAs)
   }
   // Ranks in position order (k, warp, lane), across the cluster's CTAs.
   const unsigned lt = (1u << lane) - 1u;
@@ -167,14 +176,13 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
       if (lane == 0) s_total[which] = all;
     }
     evict_sync(ctas);
-    int off = 0;
-    const uint32_t a = smem_u32(&s_total[which]);
-    for (int r = 0; r < rank; ++r) off += (int)ld_cluster_u32(mapa_shared(a, (uint32_t)r));
-    return off;
+    // lane r reads CTA r's count
+    int off = lane < rank ? (int)ld_cluster_u32(mapa_shared(smem_u32(&s_total[which]), (uint32_t)lane)) : 0;
+    return __reduce_add_sync(0xffffffffu, off);
   };
   if (eq_count == need) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) selm[k] = __ballot_sync(0xffffffffu, valid(k) && key[k] >= prefix);
+    for (int k = 0; k < kPer; ++k) selm[k] = __ballot_sync(0xffffffffu, valid(k) && (key[k] & mask) >= prefix);
   } else {
     unsigned eqm[kPer];
 #pragma unroll
@@ -282,13 +290,15 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_long_kernel(c
 }
 
 // ------------------------------------------------------------ compaction
-// A cache as planes: each a run of bytes per row, 64 rows to a page.
+// A cache as planes: each a run of bytes per row, 64 rows to a page, moved in
+// columns of 2^log2_lanes units of 16 bytes (row scales and scale blocks: one
+// unit of four or eight bytes).
 struct EvictPlane {
   uint8_t* base;
   long long page_stride;     // bytes from page to page
-  int row_stride, width;     // bytes from row to row in a page; bytes moved per row
-  int unit;                  // bytes per thread and row: 16, 8 or 4
-  int cta0;                  // first CTA (blockIdx.x) of the plane
+  int row_stride;            // bytes from row to row in a page
+  int unit, log2_lanes;      // bytes per thread, threads per row
+  int slot0;                 // first slot of the plane; a slot is a column
   int pages;                 // pages in the plane
 };
 struct CompactParams {
@@ -299,49 +309,65 @@ struct CompactParams {
   const int32_t* from;       // page table of the source
   const int32_t* to;         // of the destination (the same: in place)
   int budget, pages_from, pages_to;
-  int log2_slice;            // bytes of a row per CTA (planes of 16-byte units)
-  int chunk;                 // rows per CTA
+  int ctas;                  // CTAs per sequence and column (in place: a cluster)
 };
 
 constexpr int kCpThreads = 256;
 constexpr int kCpBatch = 8;            // rows a thread has in flight
+constexpr int kCpMaxRows = 1024;       // rows per CTA and step
 constexpr int kCpPages = 512;          // pages of a sequence held in shared memory (the rest read as needed)
+
+// a barrier of the cluster's threads that orders no memory
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 template <int kUnit> struct UnitOf;
 template <> struct UnitOf<16> { using T = uint4; };
 template <> struct UnitOf<8> { using T = uint2; };
 template <> struct UnitOf<4> { using T = uint32_t; };
 
-// Moves row kept[i] to row i, i in [lo, hi), for the byte columns [slice, slice
-// + lanes x unit) of a plane.  In place this is safe without any exchange
-// between CTAs: columns are independent, kept[i] >= i, and a CTA walks i
-// upwards in steps, writing a step's rows only after all of them are read.
-// Writing rows [i, i + R) destroys only sources that rows up to i + R - 1
-// needed, all read by then; rows read ahead of a write lie above it.
+// Moves row kept[i] to row i, i < n, for one column of a plane, in steps of
+// ctas x R rows, R per CTA.
+//
+// In place: kept[i] >= i, so writing rows [i, i + R) destroys only sources that
+// rows up to i + R - 1 needed.  A barrier per step, of the CTAs (a cluster) that
+// share the column, puts all of the step's reads before any of its writes, and
+// rows read later lie above them.  (Columns need no order among themselves.)
+// Between CTAs the barrier is a relaxed one: nothing written is read again, and
+// a thread arrives only once the values it loaded are there (it has used
+// them); a releasing barrier waits for the last step's writes too, 4 us a step.
+// With new pages nothing has to wait.
+//
 // Each step's physical rows are worked out once, by one thread per row and a
 // step ahead (kept position -> page -> row, both page tables in shared
 // memory), so the moving threads wait for one memory latency a step and
-// spend few instructions on addresses.
-template <int kUnit>
-__device__ __forceinline__ void compact_slice(const CompactParams& p, const EvictPlane& pl, const int* s_from, const int* s_to,
-                                              int2 (*s_rows)[kCpThreads * kCpBatch], int slice, int log2_lanes, int lo, int hi) {
+// spend few instructions on addresses.  Column widths, 32 x 4,096 fp8 rows and
+// keys: 64 / 128 bytes 52 / 53 us in place and 47 / 42 us into new pages; 32
+// bytes 67 / 65.  Bulk copies of whole rows through shared memory were twice
+// as slow.
+template <int kUnit, bool kInPlace>
+__device__ __forceinline__ void compact_column(const CompactParams& p, const EvictPlane& pl, const int* s_from, const int* s_to,
+                                               int2 (*s_rows)[kCpMaxRows], volatile uint32_t* s_used, int column, int n) {
   using U = typename UnitOf<kUnit>::T;
-  const int b = blockIdx.y, t = threadIdx.x;
+  constexpr int kBatch = kUnit == 16 ? kCpBatch : kCpMaxRows / kCpThreads;
+  const int b = blockIdx.y, t = threadIdx.x, rank = blockIdx.x % p.ctas;
   const int32_t* kept = p.kept + (size_t)b * p.budget;
-  const int rows = kCpThreads >> log2_lanes;        // rows per batch element
-  const int step = rows * kCpBatch;                 // rows per step (at most kCpThreads x kCpBatch)
-  const int col = slice + (t & ((1 << log2_lanes) - 1)) * kUnit, r0 = t >> log2_lanes;
-  const bool live = col < pl.width;
-  const bool in_place = p.from == p.to;
+  const int rows = kCpThreads >> pl.log2_lanes;     // rows per batch element
+  const int r0 = t >> pl.log2_lanes;
+  const int mine = rows * kBatch;                   // rows per CTA and step, at most kCpMaxRows
+  const int step = mine * p.ctas;
+  const int col = ((column << pl.log2_lanes) + (t & ((1 << pl.log2_lanes) - 1))) * kUnit;
+  const bool live = col < pl.row_stride;
   bool outside = false;
-  // (source, destination) of the rows of the step at `base`; -1: nothing moves
+  // (source, destination) of this CTA's rows of the step at `base`; -1: nothing moves
   auto prepare = [&](int base, int2* to_rows) {
-    for (int j = t; j < step; j += kCpThreads) {
-      const int i = base + j;
+    for (int j = t; j < mine; j += kCpThreads) {
+      const int i = base + rank * mine + j;
       int2 r = make_int2(-1, -1);
-      if (i < hi) {
+      if (i < n) {
         const int o = __ldg(kept + i);
-        if (o >= 0 && !(in_place && o == i)) {
+        if (o >= 0 && !(kInPlace && o == i)) {
           const int ps = o >> 6, pd = i >> 6;
           const int fp = ps < p.pages_from ? (ps < kCpPages ? s_from[ps] : __ldg(p.from + (size_t)b * p.pages_from + ps)) : -1;
           const int tp = pd < p.pages_to ? (pd < kCpPages ? s_to[pd] : __ldg(p.to + (size_t)b * p.pages_to + pd)) : -1;
@@ -352,50 +378,62 @@ __device__ __forceinline__ void compact_slice(const CompactParams& p, const Evic
       to_rows[j] = r;
     }
   };
-  prepare(lo, s_rows[0]);
+  prepare(0, s_rows[0]);
   int buf = 0;
-  for (int base = lo; base < hi; base += step, buf ^= 1) {
+  for (int base = 0; base < n; base += step, buf ^= 1) {
     __syncthreads();
-    U v[kCpBatch];
-    int to[kCpBatch];
+    U v[kBatch];
+    int to[kBatch];
 #pragma unroll
-    for (int k = 0; k < kCpBatch; ++k) {
-      const int2 r = s_rows[buf][k * rows + r0];
-      to[k] = live ? r.y : -1;
-      if (to[k] >= 0)
+    for (int k = 0; k < kBatch; ++k) {
+      const int2 r = live ? s_rows[buf][k * rows + r0] : make_int2(-1, -1);
+      to[k] = r.y;
+      if (r.y >= 0)
         v[k] = *reinterpret_cast<const U*>(pl.base + (r.x >> 6) * pl.page_stride + (uint32_t)((r.x & 63) * pl.row_stride + col));
     }
-    if (base + step < hi) prepare(base + step, s_rows[buf ^ 1]);
-    if (in_place) __syncthreads();
+    if (base + step < n) prepare(base + step, s_rows[buf ^ 1]);
+    if (kInPlace) {
+      if (p.ctas > 1) {
+        uint32_t used = 0;
 #pragma unroll
-    for (int k = 0; k < kCpBatch; ++k)
+        for (int k = 0; k < kBatch; ++k)
+          if (to[k] >= 0) used ^= *reinterpret_cast<const uint32_t*>(&v[k]);
+        s_used[t] = used;
+        __syncwarp();
+        cluster_sync_relaxed();
+      } else {
+        __syncthreads();
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
       if (to[k] >= 0)
         *reinterpret_cast<U*>(pl.base + (to[k] >> 6) * pl.page_stride + (uint32_t)((to[k] & 63) * pl.row_stride + col)) = v[k];
   }
   if (outside) atomicOr(&g_error_word, 4u);
 }
 
-__global__ void __launch_bounds__(kCpThreads) smla_evict_compact_kernel(const __grid_constant__ CompactParams p) {
+template <bool kInPlace>
+__global__ void __launch_bounds__(kCpThreads, 4) smla_evict_compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int s_from[kCpPages], s_to[kCpPages];
-  __shared__ int2 s_rows[2][kCpThreads * kCpBatch];
+  __shared__ int2 s_rows[2][kCpMaxRows];
+  __shared__ uint32_t s_used[kCpThreads];
   grid_dep_wait();
   const int b = blockIdx.y;
-  // (in place: all rows, in order; else chunks of rows)
   const int n = min(p.new_len[b], p.budget);
-  const int lo = blockIdx.z * p.chunk, hi = min(n, lo + p.chunk);
-  if (lo >= hi) return;
   for (int i = threadIdx.x; i < kCpPages; i += kCpThreads) {
     if (i < p.pages_from) s_from[i] = __ldg(p.from + (size_t)b * p.pages_from + i);
     if (i < p.pages_to) s_to[i] = __ldg(p.to + (size_t)b * p.pages_to + i);
   }
   __syncthreads();
+  const int slot = blockIdx.x / p.ctas;
   int k = p.planes - 1;
-  while ((int)blockIdx.x < p.plane[k].cta0) --k;
+  while (slot < p.plane[k].slot0) --k;
   const EvictPlane& pl = p.plane[k];
-  const int slice = ((int)blockIdx.x - pl.cta0) << p.log2_slice;
-  if (pl.unit == 16) compact_slice<16>(p, pl, s_from, s_to, s_rows, slice, p.log2_slice - 4, lo, hi);
-  else if (pl.unit == 8) compact_slice<8>(p, pl, s_from, s_to, s_rows, slice, 0, lo, hi);
-  else compact_slice<4>(p, pl, s_from, s_to, s_rows, slice, 0, lo, hi);
+  const int column = slot - pl.slot0;
+  if (pl.unit == 16) compact_column<16, kInPlace>(p, pl, s_from, s_to, s_rows, s_used, column, n);
+  else if (pl.unit == 8) compact_column<8, kInPlace>(p, pl, s_from, s_to, s_rows, s_used, column, n);
+  else compact_column<4, kInPlace>(p, pl, s_from, s_to, s_rows, s_used, column, n);
 }
 
 // ------------------------------------------------------------------ host
@@ -475,28 +513,32 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
   const int sms = device_sm_count();
   if (sms <= 0) return SMLA_ERR_CUDA;
   const bool in_place = !new_page_table || new_page_table == page_table;
-  // In place a CTA walks all rows of its slice, so few sequences need narrow
-  // slices to spread over the device; new pages are also split by rows.
-  const int row_bytes = s->kv_dtype == SMLA_KV_BF16 ? kRowBytesBf16 : kRowBytesFp8;
-  p.log2_slice = 7;
-  while (in_place && p.log2_slice > 5 && (long long)s->batch * (row_bytes >> p.log2_slice) < sms) --p.log2_slice;
-  p.chunk = in_place ? s->budget : (kCpThreads >> (p.log2_slice - 4)) * kCpBatch;
-  int ctas = 0;
-  auto plane = [&](void* base, long long page_stride, int row_stride, int width, int unit, long long rows) {
-    EvictPlane& pl = p.plane[p.planes++];
-    pl = {static_cast<uint8_t*>(base), page_stride, row_stride, width, unit, ctas, (int)(rows / 64)};
-    ctas += unit == 16 ? (width + (1 << p.log2_slice) - 1) >> p.log2_slice : 1;
+  const int log2_lanes = in_place ? 2 : 3;          // columns of 64 or 128 bytes
+  int slots = 0;
+  auto plane = [&](void* base, long long page_stride, int row_stride, int unit, long long rows) {
+    const int lg = unit == 16 ? log2_lanes : 0;
+    p.plane[p.planes++] = {static_cast<uint8_t*>(base), page_stride, row_stride, unit, lg, slots, (int)(rows / 64)};
+    slots += (row_stride + (unit << lg) - 1) / (unit << lg);
   };
   if (s->kv_dtype == SMLA_KV_BF16) {
-    plane(kv, 64ll * kRowBytesBf16, kRowBytesBf16, kRowBytesBf16, 16, s->num_kv_rows);
+    plane(kv, 64ll * kRowBytesBf16, kRowBytesBf16, 16, s->num_kv_rows);
   } else if (s->kv_dtype == SMLA_KV_FP8_E4M3_ROWSCALE) {
-    plane(kv, 64ll * kRowBytesFp8, kRowBytesFp8, kRowBytesFp8, 16, s->num_kv_rows);
-    plane(kv_row_scale, 64 * 4, 4, 4, 4, s->num_kv_rows);
+    plane(kv, 64ll * kRowBytesFp8, kRowBytesFp8, 16, s->num_kv_rows);
+    plane(kv_row_scale, 64 * 4, 4, 4, s->num_kv_rows);
   } else {
-    plane(kv, kDsv4Page, kDsv4Slot, kDsv4Slot, 16, s->num_kv_rows);
-    plane(static_cast<uint8_t*>(kv) + kDsv4ScaleOff, kDsv4Page, 8, 8, 8, s->num_kv_rows);
+    plane(kv, kDsv4Page, kDsv4Slot, 16, s->num_kv_rows);
+    plane(static_cast<uint8_t*>(kv) + kDsv4ScaleOff, kDsv4Page, 8, 8, s->num_kv_rows);
   }
-  if (k_cache) plane(k_cache, 64 * 256, 256, 256, 16, s->num_key_rows);
+  if (k_cache) plane(k_cache, 64 * 256, 256, 16, s->num_key_rows);
+  // In place a cluster per column: as many CTAs (a power of two, at most eight)
+  // as leave three to an SM.  New pages: a CTA per step.
+  const int step_rows = (kCpThreads >> log2_lanes) * kCpBatch;
+  p.ctas = 1;
+  if (in_place) {
+    while (p.ctas < 8 && (long long)s->batch * slots * p.ctas * 2 <= 3 * sms && s->budget > step_rows * p.ctas) p.ctas *= 2;
+  } else {
+    p.ctas = (s->budget + step_rows - 1) / step_rows;
+  }
   p.kept = kept;
   p.new_len = new_len;
   p.from = page_table;
@@ -504,11 +546,21 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
   p.budget = s->budget;
   p.pages_from = s->pages_per_seq;
   p.pages_to = p.to == p.from ? s->pages_per_seq : s->new_pages_per_seq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(slots * p.ctas), (unsigned)s->batch);
+  cfg.blockDim = dim3(kCpThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)p.ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = in_place && p.ctas > 1 ? 2 : 1;
   void* args[] = {&p};
-  const cudaError_t e = launch_pdl((const void*)smla_evict_compact_kernel, dim3((unsigned)ctas, (unsigned)s->batch,
-                                                                                   (unsigned)((s->budget + p.chunk - 1) / p.chunk)),
-                                   dim3(kCpThreads), 0, stream, args);
-  return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
+  const void* kern = in_place ? (const void*)smla_evict_compact_kernel<true> : (const void*)smla_evict_compact_kernel<false>;
+  return cudaLaunchKernelExC(&cfg, kern, args) == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
 }  // namespace smla
