@@ -308,7 +308,8 @@ def _plan_rope(api, s):
 def _plan_append(api, s):
     rope = api.RopeTable(**_rope_arguments(s["rope"])) if s["rope"] else None
     return api.CacheAppendPlan(s["x"], s["kv"], s["slots"], kv_row_scale=s["kv_row_scale"], page_table=s["page_table"],
-                               page_size=0 if s["page_table"] is None else PAGE, seq=s["seq"],
+                               page_size=0 if s["page_table"] is None else PAGE,
+                               seq=None if s["page_table"] is None else s["seq"],
                                norm_weight=s["norm_weight"], eps=1e-6, rope=rope,
                                positions=s["positions"] if rope else None)
 
