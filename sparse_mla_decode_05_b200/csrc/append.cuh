@@ -50,6 +50,29 @@ __device__ __forceinline__ RopeVec<T, 8> ap_load8(const T* src) {
   }
   return r;
 }
+// two fp32 at a time (the packed instructions issue once for both)
+__device__ __forceinline__ void ap_mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1) : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void ap_fma2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
+      "fma.rn.f32x2 d, a, b, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void ap_scale8(float (&v)[8], float s) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) ap_mul2(v[j], v[j + 1], s, s);
+}
+__device__ __forceinline__ void ap_mul8(float (&v)[8], const float (&w)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) ap_mul2(v[j], v[j + 1], w[j], w[j + 1]);
+}
+__device__ __forceinline__ float ap_rcp(float x) {     // within one ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // eight fp32 -> eight e4m3 codes
 __device__ __forceinline__ uint2 ap_codes8(const float (&v)[8]) {
   return make_uint2(pack_e4m3x2(v[0], v[1]) | (pack_e4m3x2(v[2], v[3]) << 16),
@@ -167,19 +190,20 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
     rope_unpack<T, 8>(x1, v1);
     float a = RopeIo<T>::get(xa), b = RopeIo<T>::get(xb), r = 1.f;
     if (p.norm_weight) {
-      float ss = 0.f;
+      float ss = 0.f, ss1 = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v0[j], v0[j], fmaf(v1[j], v1[j], ss));
+      for (int j = 0; j < 8; j += 2) {
+        ap_fma2(ss, ss1, v0[j], v0[j + 1], v0[j], v0[j + 1]);
+        ap_fma2(ss, ss1, v1[j], v1[j + 1], v1[j], v1[j + 1]);
+      }
+      ss += ss1;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
       // (1 / rms goes to the row's largest value and to the final scaling of
       // fp8 rows, not to every element on the way)
       r = rsqrtf(ss * (1.0f / 512.0f) + p.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v0[j] *= w0[j];
-        v1[j] *= w1[j];
-      }
+      ap_mul8(v0, w0);
+      ap_mul8(v1, w1);
       if (kDsv4) {
         a = a * r * wa;
         b = b * r * wb;
@@ -194,10 +218,9 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
     }
     if constexpr (kKind == kKindBf16) {
       __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.kv) + row * kDqk;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v0[j] *= r;
-        v1[j] *= r;
+      if (p.norm_weight) {
+        ap_scale8(v0, r);
+        ap_scale8(v1, r);
       }
       *reinterpret_cast<uint4*>(dst + 8 * lane) = make_uint4(pack_bf16x2(v0[0], v0[1]), pack_bf16x2(v0[2], v0[3]),
                                                              pack_bf16x2(v0[4], v0[5]), pack_bf16x2(v0[6], v0[7]));
@@ -210,24 +233,44 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
         dst[db] = __float2bfloat16_rn(b);
       }
     } else if constexpr (kKind == kKindFp8) {
-      float m = fmaxf(fmaxf(ap_amax8(v0), ap_amax8(v1)) * r, fmaxf(fabsf(a), fabsf(b)));
       // (magnitudes order as their bits do)
-      m = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(m)));
+      const float latent = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(fmaxf(ap_amax8(v0), ap_amax8(v1)))));
+      const float rope = __int_as_float(__reduce_max_sync(0xffffffffu, __float_as_int(fmaxf(fabsf(a), fabsf(b)))));
+      const float m = fmaxf(latent * r, rope);
       // a row of zeros keeps scale 1; a scale below the normal range would
       // lose bits, so it stops at 2^-126
-      const float scale = m > 0.f ? fmaxf(__fdiv_rn(m, 448.0f), 1.1754943508222875e-38f) : 1.0f;
+      // (m / 448 by its remainder: correctly rounded)
+      const float m448 = m * (1.0f / 448.0f);
+      const float scale = m > 0.f ? fmaxf(fmaf(fmaf(-m448, 448.0f, m), 1.0f / 448.0f, m448), 1.1754943508222875e-38f) : 1.0f;
       uint8_t* dst = p.kv + row * kRowBytesFp8;
-      // the quotient by way of the reciprocal: within 2^-22 of x / scale, far
-      // inside the half step of 2^-4 that the codes round by
-      const float inv = __frcp_rn(scale), rinv = r * inv;
+      // x / scale.  Normalised values: by way of the reciprocal (of the largest
+      // of them, where that sets the scale: 1 / rms then cancels), within
+      // 2^-22, far inside the half step of 2^-4 that the codes round by.  Values as
+      // they came have few bits, and can lie on the border between two codes
+      // exactly: their quotient is made exact there by its remainder.
+      const float inv = ap_rcp(scale);
+      auto exact = [&](float x) -> float {
+        const float q = x * inv;
+        return fmaf(fmaf(-q, scale, x), inv, q);
+      };
+      if (p.norm_weight) {
+        float rinv = r * inv;
+        if (latent * r >= rope && scale > 1.1754943508222875e-38f && m > 0.f) {
+          const float y = ap_rcp(latent);
+          rinv = 448.0f * fmaf(fmaf(-latent, y, 1.0f), y, y);
+        }
+        ap_scale8(v0, rinv);
+        ap_scale8(v1, rinv);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v0[j] *= rinv;
-        v1[j] *= rinv;
+        for (int j = 0; j < 8; ++j) {
+          v0[j] = exact(v0[j]);
+          v1[j] = exact(v1[j]);
+        }
       }
       *reinterpret_cast<uint2*>(dst + 8 * lane) = ap_codes8(v0);
       *reinterpret_cast<uint2*>(dst + 256 + 8 * lane) = ap_codes8(v1);
-      const uint32_t ab = pack_e4m3x2(a * inv, b * inv);
+      const uint32_t ab = pack_e4m3x2(exact(a), exact(b));
       if (inter) {
         *reinterpret_cast<uint16_t*>(dst + da) = (uint16_t)ab;
       } else {

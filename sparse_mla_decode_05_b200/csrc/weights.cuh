@@ -34,7 +34,16 @@ struct WtCfg {
   static constexpr int kQHeads = kH / kQWarps;
   static constexpr int kQRows = kFp8 ? 128 : 64;                   // fp8: the heads' high parts, then their low parts
   static constexpr int kQBytes = kQRows * kRowBytes;
-  static constexpr int kN = kQRows;                                // MMA N: columns of a score buffer
+  static constexpr int kMmaN = kQRows;
+  // bf16 operands: the K steps go to four accumulators, added in the epilogue.
+  // The tensor cores cut every update of an accumulator to fp32, an error in
+  // proportion to its value and all of one sign; in a quarter each, partial
+  // sums are a quarter as large (one sequence, scores up to 20: relative
+  // error of the weights 7.7e-6 with one accumulator, 1.4e-6 with four; 1 % of
+  // the time).  DeepSeek-V4 rows, short of registers, take two; fp8 rows take
+  // half the steps, in two parts already.
+  static constexpr int kAccs = kFp8 ? 1 : (kKind == kKindBf16 ? 4 : 2);
+  static constexpr int kN = kAccs * kMmaN;                         // columns of a score buffer
   static constexpr uint32_t kTmem = 2 * kN;
   static constexpr int kSmemQ = kStages * kStageBytes;
   static constexpr int kSmemRow = kSmemQ + kQBytes;                // int  [kWtRing][kM] physical row or -1
@@ -291,8 +300,10 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
 #pragma unroll
         for (int k = 0; k < C::kQK / 16; ++k) {
           const uint64_t off = (uint64_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
-          if (k == 0) mma_set_elect(d, da, db, idesc);
-          else mma_acc_elect(d, da + off, db + off, idesc);
+          constexpr int kPart = C::kQK / 16 / C::kAccs;                // K steps per accumulator
+          const uint32_t dk = d + (uint32_t)(k / kPart * C::kMmaN);
+          if (k % kPart == 0) mma_set_elect(dk, da + off, db + off, idesc);
+          else mma_acc_elect(dk, da + off, db + off, idesc);
         }
       }
       commit_elect(BAR(WB_EMPTY + stage));
@@ -373,11 +384,20 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
             sum += weigh(x, lse + 16 * g, kh + 16 * g);
           }
         } else {
-          float x[32];
-          tmem_ld_16x32bx2_x32(d, x);
-          tmem_wait_ld();
-          taken();
-          sum = weigh(x, lse, kh) + weigh(x + 16, lse + 16, kh + 16);
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float x[16], y[16];
+            tmem_ld_16x32bx2_x16(d + 16u * (uint32_t)g, x);
+#pragma unroll
+            for (int a = 1; a < C::kAccs; ++a) {
+              tmem_ld_16x32bx2_x16(d + (uint32_t)(a * C::kMmaN) + 16u * (uint32_t)g, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int h = 0; h < 16; ++h) x[h] += y[h];
+            }
+            if (g == 1) taken();
+            sum += weigh(x, lse + 16 * g, kh + 16 * g);
+          }
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         }
         const int at = tin * kM + e;
