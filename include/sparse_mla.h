@@ -492,8 +492,9 @@ typedef struct {
  * With transpose the call is the gradient of the rotation with respect to x
  * (x is then the gradient of y), which undoes the rotation when mscale = 1:
  * DeepSeek-V4 rows carry rotated dims in the value too, and its output's
- * last 64 dims are turned back this way.  Rows of y may not share memory
- * (SMLA_ERR_INVALID_ARG where the strides say so). */
+ * last 64 dims are turned back this way.  Rows of y may not share memory: one
+ * of its strides clears all the rows along the other (else
+ * SMLA_ERR_INVALID_ARG). */
 smla_status sparse_mla_rope(const smla_rope_shape* shape, const smla_rope_table* table, const void* x,
                             const int32_t* positions, void* y, void* stream);
 

@@ -253,9 +253,17 @@ static cudaError_t launch_rope(RopeParams p, const smla_rope_shape* s, bool inte
   return inter ? launch_rope_as<T, 1, true>(p, s->tokens, stream) : launch_rope_as<T, 1, false>(p, s->tokens, stream);
 }
 
-// |stride| keeps rows of `width` elements apart (a dim of size one has none)
-static bool apart(long long stride, long long size, int width) {
-  return size <= 1 || stride >= width || stride <= -(long long)width;
+// Rows of `width` elements at two strides share no memory: one dim's stride
+// clears all that the other one spans (a dim of size one spans nothing).
+static bool rows_apart(long long s0, long long n0, long long s1, long long n1, int width) {
+  const long long a0 = s0 < 0 ? -s0 : s0, a1 = s1 < 0 ? -s1 : s1;
+  const long long most = 1ll << 62;
+  auto span = [&](long long stride, long long n) -> long long {     // of n rows
+    return stride > 0 && n - 1 > (most - width) / stride ? most : (n - 1) * stride + width;
+  };
+  if (n0 <= 1) return n1 <= 1 || a1 >= width;
+  if (n1 <= 1) return a0 >= width;
+  return (a1 >= width && a0 >= span(a1, n1)) || (a0 >= width && a1 >= span(a0, n0));
 }
 
 static smla_status run_rope(const smla_rope_shape* s, const smla_rope_table* t, const void* x, const int32_t* positions,
@@ -271,10 +279,9 @@ static smla_status run_rope(const smla_rope_shape* s, const smla_rope_table* t, 
   const int size = dtype_bytes(s->dtype);
   if (!x || !y || !positions || !aligned(x, size) || !aligned(y, size) || !aligned(positions, 4))
     return SMLA_ERR_INVALID_ARG;
-  // rows of y do not meet (a stride of zero, or below the width, would have
-  // two rows written to one place); in place the layouts are the same
-  if (!apart(s->y_token_stride, s->tokens, s->dim) || !apart(s->y_head_stride, s->heads, s->dim))
-    return SMLA_ERR_INVALID_ARG;
+  // rows of y do not meet (two would be written to one place); in place the
+  // layouts are the same
+  if (!rows_apart(s->y_token_stride, s->tokens, s->y_head_stride, s->heads, s->dim)) return SMLA_ERR_INVALID_ARG;
   const bool in_place = x == y;
   if (in_place && ((s->tokens > 1 && s->x_token_stride != s->y_token_stride) ||
                    (s->heads > 1 && s->x_head_stride != s->y_head_stride)))

@@ -81,7 +81,8 @@ def test_rope_refusals():
     t = _table()
     for kw in (dict(tokens=-1), dict(heads=0), dict(heads=65537), dict(dim=1), dict(dim=63), dict(offset=1),
                dict(offset=-1), dict(transpose=2), dict(reserved=1), dict(y_head_stride=0), dict(y_head_stride=63),
-               dict(y_token_stride=0)):
+               dict(y_token_stride=0), dict(y_token_stride=127), dict(y_token_stride=64), dict(y_head_stride=128),
+               dict(y_head_stride=-63), dict(tokens=1, y_head_stride=63), dict(heads=1, y_token_stride=63)):
         assert f(_rope_shape(**kw), t, 16, 16, 32, None) == INVALID, kw
     assert f(_rope_shape(dtype=3), t, 16, 16, 32, None) == UNSUPPORTED
     assert f(None, t, 16, 16, 32, None) == INVALID and f(_rope_shape(), None, 16, 16, 32, None) == INVALID
@@ -90,6 +91,7 @@ def test_rope_refusals():
     assert f(_rope_shape(dtype=2), t, 18, 16, 32, None) == INVALID           # fp32 elements need 4 bytes
     assert f(_rope_shape(x_token_stride=256), t, 32, 16, 32, None) == INVALID   # in place with other strides
     assert f(_rope_shape(tokens=0), t, None, None, None, None) == 0           # nothing to do
+    assert f(_rope_shape(tokens=0, y_head_stride=64, y_token_stride=128), t, None, None, None, None) == 0
     bad = api.RopeTableData()
     assert f(_rope_shape(), ctypes.byref(bad), 16, 16, 32, None) == INVALID
 
