@@ -121,17 +121,18 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      // keys of one value (weights of zero, protected positions) would queue
-      // at one counter: one atomic for the warp where all its keys agree
+      // weights of zero and protected positions, which may be most, would queue
+      // at one counter each: one atomic for those of a warp
       const bool in = valid(k) && (key[k] & mask) == prefix;
       const uint32_t digit = (key[k] >> shift) & dmask;
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (!in) continue;
-      const int first = __ffs(act) - 1;
-      const uint32_t d0 = __shfl_sync(act, digit, first);
-      const unsigned same = __ballot_sync(act, digit == d0);
-      if (digit != d0) atomicAdd(&h[digit], 1u);
-      else if (lane == first) atomicAdd(&h[digit], (uint32_t)__popc(same));
+      const bool zero = in && key[k] == 0x80000000u, fixed = in && key[k] == 0xFFFFFFFFu;
+      const unsigned zeros = __ballot_sync(0xffffffffu, zero), fixeds = __ballot_sync(0xffffffffu, fixed);
+      if (zero || fixed) {
+        const unsigned same = zero ? zeros : fixeds;
+        if (lane == __ffs(same) - 1) atomicAdd(&h[digit], (uint32_t)__popc(same));
+      } else if (in) {
+        atomicAdd(&h[digit], 1u);
+      }
     }
     evict_sync(ctas);
     if (ctas > 1) {
