@@ -398,7 +398,9 @@ __device__ __forceinline__ void compact_column(const CompactParams& p, const Evi
         uint32_t used = 0;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k)
-          if (to[k] >= 0) used ^= *reinterpret_cast<const uint32_t*>(&v[k]);
+          if (to[k] >= 0)
+#pragma unroll
+            for (int w = 0; w < kUnit / 4; ++w) used ^= reinterpret_cast<const uint32_t*>(&v[k])[w];
         s_used[t] = used;
         __syncwarp();
         cluster_sync_relaxed();

@@ -582,13 +582,14 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
   for (int i = t; i < kAcRange / 32; i += kAcThreads) bad[i] = 0;
   if (t == 0) s_max = 0;
   __syncthreads();
-  // largest finite |weight| (as bits) of the sequence's entries
+  // largest finite |weight| (as bits) of the sequence's entries; at least the
+  // smallest number where any entry is NaN or infinite
   int m = 0;
   bool outside = false;
   for (int i = t; i < p.entries; i += kAcThreads) {
     const int at = __ldg(idx + i), v = __float_as_int(fabsf(__ldg(w + i)));
     outside |= at >= p.max_ctx;
-    if (at >= 0 && at < p.max_ctx && v < 0x7F800000) m = max(m, v);
+    if (at >= 0 && at < p.max_ctx) m = max(m, v < 0x7F800000 ? v : 1);
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if ((t & 31) == 0 && m > 0) atomicMax(&s_max, m);

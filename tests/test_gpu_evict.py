@@ -125,6 +125,27 @@ def test_long_contexts(n, budget):
         assert torch.equal(kv[row(tail)], old[row(tail)])
 
 
+@pytest.mark.parametrize("n,budget", [(131072, 131000), (131073, 60000), (300000, 299990)])
+def test_long_selection_in_place(n, budget):
+    """The accumulated weights and the lengths overwritten in place, on both sides of the border between the two kernels."""
+    g = torch.Generator("cuda").manual_seed(n)
+    acc = torch.round(torch.rand(1, n, generator=g, device="cuda") * 50)
+    ctx = torch.tensor([n], dtype=torch.int32, device="cuda")
+    pps = -(-n // 64)
+    pt = torch.arange(pps, dtype=torch.int32, device="cuda")[None]
+    kv, rs = random_cache("fp8", pps * 64, 6)
+    old, old_rs, before = kv.clone(), rs.clone(), acc.clone()
+    kept, new_len, out = api().evict(acc, ctx, budget, page_table=pt, kv=kv, kv_row_scale=rs, recent=3, new_len=ctx)
+    assert out is acc and new_len is ctx and ctx.item() == budget
+    key = before[0].clone()
+    key[n - 3:] = torch.inf
+    sel = torch.sort(key, descending=True, stable=True).indices[:budget].sort().values
+    assert torch.equal(kept[0].long(), sel)
+    assert torch.equal(acc[0, :budget], before[0][sel]) and torch.all(acc[0, budget:] == 0)
+    assert torch.equal(kv[:budget], old[sel]) and torch.equal(rs[:budget], old_rs[sel])
+    assert torch.equal(kv[budget:], old[budget:])
+
+
 def test_context_and_pages_out_of_range():
     acc = torch.rand(2, 128, device="cuda")
     kv, _ = random_cache("bf16", 256, 4)

@@ -251,6 +251,16 @@ def test_accumulate_nan_and_infinite_weights_stay_at_their_position():
     assert np.isnan(got[0]) and np.isnan(got[1]) and got[2] == 3.0 and np.all(got[4:] == 0)
 
 
+@pytest.mark.parametrize("decay", [1.0, 0.5])
+def test_accumulate_nothing_but_nan_and_infinity(decay):
+    acc = torch.ones(1, 5000, device="cuda")
+    idx = torch.tensor([[7, 4999, 30, -1]], dtype=torch.int32, device="cuda")
+    w = torch.tensor([[float("nan"), -float("inf"), 0.0, float("nan")]], device="cuda")
+    api().accumulate_weights(acc, idx, w, decay=decay)
+    got = acc.cpu().numpy()[0]
+    assert np.isnan(got[7]) and np.isnan(got[4999]) and np.all(np.delete(got, [7, 4999]) == decay)
+
+
 def test_accumulate_all_zero_or_no_weights_still_decays():
     acc = torch.ones(2, 5000, device="cuda")
     api().accumulate_weights(acc, torch.full((2, 3), -1, dtype=torch.int32, device="cuda"), torch.ones(2, 3, device="cuda"), decay=0.5)
