@@ -4,7 +4,8 @@
 
 namespace smla {
 
-constexpr int kEvThreads = 1024;       // selection: one CTA per sequence
+constexpr int kEvThreads = 1024;       // selection
+constexpr int kEvPer = 8;              // weights per thread and tile
 
 static_assert(sizeof(smla_evict_shape) == 48 && offsetof(smla_evict_shape, num_kv_rows) == 32, "smla_evict_shape layout");
 
@@ -23,14 +24,17 @@ __device__ __forceinline__ uint32_t evict_key(float w, int i, int sinks, int tai
   return w == w ? order_key(w) : 0u;
 }
 
-// Contexts up to kEvMaxCtas x 16,384 positions: a cluster of CTAs per
-// sequence, every thread holding kPer of its weights in registers, so that
-// the weights are read once and acc_out may be acc.  Radix select of the
-// budget-th largest key by digits of 11, 11 and 10 bits: each CTA counts its
-// keys in shared memory, all read the counts of all (distributed shared
-// memory), and pick the same digit.  Then every key above the selection is
-// kept and the lowest positions equal to it; the CTAs exchange their counts to
-// know where their kept positions go.
+// A cluster of CTAs per sequence, each thread holding eight weights of a tile of
+// ctas x 8,192 positions.  Radix select of the budget-th largest key by digits
+// of 11, 11 and 10 bits: each CTA counts its keys in shared memory, all read
+// the counts of all (distributed shared memory), and pick the same digit; it
+// ends as soon as all keys that start with the digits so far are kept.  Then
+// every key above the selection is kept and the lowest positions equal to it;
+// the CTAs exchange their counts to know where their kept positions go.
+// Contexts of one tile (65,536 positions with eight CTAs) read the weights
+// once; longer ones read them again for each digit and for the compaction,
+// which walks the tiles upwards and writes, once all CTAs have read a tile, at
+// or below where it was read: acc_out may be acc.
 constexpr int kEvMaxCtas = 8;          // the portable cluster size
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -68,13 +72,13 @@ __device__ __forceinline__ int prefix_counts(int* v) {
   return __shfl_sync(0xffffffffu, incl, 31);
 }
 
-template <int kPer>
+template <bool kLong>     // more than one tile
 __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const SelectParams p) {
   __shared__ uint32_t hist[2][2048];
   __shared__ uint32_t total[2048];
-  __shared__ int cnt[32 * kPer];      // [k][warp] counts, then their prefix sums
+  __shared__ int cnt[32 * kEvPer];    // [k][warp] counts, then their prefix sums
   __shared__ int wsum[32];
-  __shared__ int s_total[2];          // this CTA's keys equal to the selection, and its kept keys
+  __shared__ int s_total[2][2];       // [tile parity]: this CTA's keys equal to the selection, and its kept keys
   __shared__ uint32_t s_digit;
   __shared__ int s_need, s_cnt;
   grid_dep_wait();
@@ -89,7 +93,6 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
   const float* acc = p.acc + (size_t)b * p.max_ctx;
   float* out = p.acc_out + (size_t)b * p.max_ctx;
   int32_t* kept = p.kept + (size_t)b * p.budget;
-  const int base = rank * kEvThreads * kPer;
   if (n <= p.budget) {
     for (int i = rank * kEvThreads + t; i < p.budget; i += ctas * kEvThreads) kept[i] = i < n ? i : -1;
     if (out != acc)
@@ -99,16 +102,19 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
     if (rank == 0 && t == 0) p.new_len[b] = n;
     return;
   }
-  const int tail = n - p.recent;
-  float w[kPer];
-  uint32_t key[kPer];
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = base + k * kEvThreads + t;
-    w[k] = i < n ? acc[i] : 0.f;
-    key[k] = evict_key(w[k], i, p.sinks, tail);
-  }
+  const int tail = n - p.recent, tile = ctas * kEvThreads * kEvPer;
+  float w[kEvPer];
+  uint32_t key[kEvPer];
+  int base = 0;                       // this CTA's first position of the tile at hand
   auto valid = [&](int k) -> bool { return base + k * kEvThreads + t < n; };
+  auto load = [&](int first) {
+    base = first + rank * kEvThreads * kEvPer;
+#pragma unroll
+    for (int k = 0; k < kEvPer; ++k) w[k] = valid(k) ? acc[base + k * kEvThreads + t] : 0.f;
+#pragma unroll
+    for (int k = 0; k < kEvPer; ++k) key[k] = evict_key(w[k], base + k * kEvThreads + t, p.sinks, tail);
+  };
+  load(0);
   uint32_t prefix = 0, mask = 0;
   int need = p.budget, eq_count = 0;
 #pragma unroll 1
@@ -119,19 +125,23 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
     h[t] = 0;
     h[t + 1024] = 0;
     __syncthreads();
+#pragma unroll 1
+    for (int first = 0; first < (kLong ? n : 1); first += tile) {
+      if (kLong && (pass > 0 || first > 0)) load(first);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      // weights of zero and protected positions, which may be most, would queue
-      // at one counter each: one atomic for those of a warp
-      const bool in = valid(k) && (key[k] & mask) == prefix;
-      const uint32_t digit = (key[k] >> shift) & dmask;
-      const bool zero = in && key[k] == 0x80000000u, fixed = in && key[k] == 0xFFFFFFFFu;
-      const unsigned zeros = __ballot_sync(0xffffffffu, zero), fixeds = __ballot_sync(0xffffffffu, fixed);
-      if (zero || fixed) {
-        const unsigned same = zero ? zeros : fixeds;
-        if (lane == __ffs(same) - 1) atomicAdd(&h[digit], (uint32_t)__popc(same));
-      } else if (in) {
-        atomicAdd(&h[digit], 1u);
+      for (int k = 0; k < kEvPer; ++k) {
+        // weights of zero and protected positions, which may be most, would
+        // queue at one counter each: one atomic for those of a warp
+        const bool in = valid(k) && (key[k] & mask) == prefix;
+        const uint32_t digit = (key[k] >> shift) & dmask;
+        const bool zero = in && key[k] == 0x80000000u, fixed = in && key[k] == 0xFFFFFFFFu;
+        const unsigned zeros = __ballot_sync(0xffffffffu, zero), fixeds = __ballot_sync(0xffffffffu, fixed);
+        if (zero || fixed) {
+          const unsigned same = zero ? zeros : fixeds;
+          if (lane == __ffs(same) - 1) atomicAdd(&h[digit], (uint32_t)__popc(same));
+        } else if (in) {
+          atomicAdd(&h[digit], 1u);
+        }
       }
     }
     evict_sync(ctas);
@@ -163,131 +173,70 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
     __syncthreads();
     if (eq_count == need) break;      // every key that starts with these digits is kept (the same in all CTAs)
   }
-  // Ranks in position order (k, warp, lane), across the cluster's CTAs.
+  // Ranks in position order (k, warp, lane) and across the cluster's CTAs.
+  // cnt receives the CTA's exclusive counts; returns what the lower CTAs count,
+  // *all what the whole tile does.
   const unsigned lt = (1u << lane) - 1u;
-  unsigned selm[kPer];
-  auto ranks = [&](const unsigned (&m)[kPer], int which) -> int {   // cnt: exclusive counts; returns the CTA's offset
+  auto ranks = [&](const unsigned (&m)[kEvPer], int* slot, int* all) -> int {
     if (lane == 0) {
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) cnt[k * 32 + warp] = __popc(m[k]);
+      for (int k = 0; k < kEvPer; ++k) cnt[k * 32 + warp] = __popc(m[k]);
     }
     __syncthreads();
     if (warp == 0) {
-      const int all = prefix_counts<kPer>(cnt);
-      if (lane == 0) s_total[which] = all;
+      const int sum = prefix_counts<kEvPer>(cnt);
+      if (lane == 0) *slot = sum;
     }
     evict_sync(ctas);
     // lane r reads CTA r's count
-    int off = lane < rank ? (int)ld_cluster_u32(mapa_shared(smem_u32(&s_total[which]), (uint32_t)lane)) : 0;
-    return __reduce_add_sync(0xffffffffu, off);
+    const int c = lane < ctas ? (int)ld_cluster_u32(mapa_shared(smem_u32(slot), (uint32_t)lane)) : 0;
+    *all = __reduce_add_sync(0xffffffffu, c);
+    return __reduce_add_sync(0xffffffffu, lane < rank ? c : 0);
   };
-  if (eq_count == need) {
+  int written = 0, ties = 0;          // kept, and equal to the selection, in the tiles before
+  unsigned selm[kEvPer];
+#pragma unroll 1
+  for (int first = 0, turn = 0; first < (kLong ? n : 1); first += tile, turn ^= 1) {
+    if (kLong) load(first);
+    int all;
+    if (eq_count == need) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) selm[k] = __ballot_sync(0xffffffffu, valid(k) && (key[k] & mask) >= prefix);
-  } else {
-    unsigned eqm[kPer];
+      for (int k = 0; k < kEvPer; ++k) selm[k] = __ballot_sync(0xffffffffu, valid(k) && (key[k] & mask) >= prefix);
+    } else {
+      unsigned eqm[kEvPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) eqm[k] = __ballot_sync(0xffffffffu, valid(k) && key[k] == prefix);
-    const int off = ranks(eqm, 0);
+      for (int k = 0; k < kEvPer; ++k) eqm[k] = __ballot_sync(0xffffffffu, valid(k) && key[k] == prefix);
+      const int off = ties + ranks(eqm, &s_total[turn][0], &all);
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int rk = off + cnt[k * 32 + warp] + __popc(eqm[k] & lt);
-      selm[k] = __ballot_sync(0xffffffffu, valid(k) && (key[k] > prefix || (key[k] == prefix && rk < need)));
-    }
-    __syncthreads();   // every rank read before cnt is reused
-  }
-  const int off = ranks(selm, 1);   // (all CTAs have read their weights by here)
-#pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = base + k * kEvThreads + t;
-    if ((selm[k] >> lane) & 1u) {
-      const int pos = off + cnt[k * 32 + warp] + __popc(selm[k] & lt);
-      if (pos < p.budget) {
-        kept[pos] = i;
-        out[pos] = w[k];
+      for (int k = 0; k < kEvPer; ++k) {
+        const int rk = off + cnt[k * 32 + warp] + __popc(eqm[k] & lt);
+        selm[k] = __ballot_sync(0xffffffffu, valid(k) && (key[k] > prefix || (key[k] == prefix && rk < need)));
       }
+      ties += all;
+      __syncthreads();   // every rank read before cnt is reused
     }
-    if (i >= p.budget && i < n) out[i] = 0.f;
+    const int off = written + ranks(selm, &s_total[turn][1], &all);   // (all CTAs have read the tile by here)
+#pragma unroll
+    for (int k = 0; k < kEvPer; ++k) {
+      const int i = base + k * kEvThreads + t;
+      if ((selm[k] >> lane) & 1u) {
+        const int pos = off + cnt[k * 32 + warp] + __popc(selm[k] & lt);
+        if (pos < p.budget) {
+          kept[pos] = i;
+          out[pos] = w[k];
+        }
+      }
+      if (!kLong && i >= p.budget && i < n) out[i] = 0.f;
+    }
+    written += all;
+    if (kLong) __syncthreads();       // cnt read before the next tile counts
+  }
+  if (kLong) {
+    evict_sync(ctas);                 // every tile read before the rest is cleared
+    for (int i = p.budget + rank * kEvThreads + t; i < n; i += ctas * kEvThreads) out[i] = 0.f;
   }
   if (rank == 0 && t == 0) p.new_len[b] = p.budget;
   if (ctas > 1) cluster_sync_all();   // no CTA leaves while its counts may be read
-}
-
-// Longer contexts: one CTA per sequence re-reads the weights, four digits of
-// eight bits, then a compaction of 1,024 positions at a time that walks
-// upwards and writes at or below where it reads, so acc_out may be acc.
-__global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_long_kernel(const SelectParams p) {
-  __shared__ uint32_t hist[256];
-  __shared__ int sums[65];
-  __shared__ uint32_t s_digit;
-  __shared__ int s_need;
-  grid_dep_wait();
-  const int b = blockIdx.x, t = threadIdx.x, lane = t & 31;
-  int n = p.ctx_len[b];
-  if (n < 0 || n > p.max_ctx) {
-    if (t == 0) atomicOr(&g_error_word, 4u);
-    n = n < 0 ? 0 : p.max_ctx;
-  }
-  const float* acc = p.acc + (size_t)b * p.max_ctx;
-  float* out = p.acc_out + (size_t)b * p.max_ctx;
-  int32_t* kept = p.kept + (size_t)b * p.budget;
-  __syncthreads();       // ctx_len read by all before new_len (which may be it) is written
-  if (n <= p.budget) {
-    for (int i = t; i < p.budget; i += kEvThreads) kept[i] = i < n ? i : -1;
-    if (out != acc)
-      for (int i = t; i < n; i += kEvThreads) out[i] = acc[i];
-    if (t == 0) p.new_len[b] = n;
-    return;
-  }
-  const int tail = n - p.recent;
-  uint32_t prefix = 0, mask = 0;
-  int need = p.budget;
-#pragma unroll 1
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    if (t < 256) hist[t] = 0;
-    __syncthreads();
-#pragma unroll 1
-    for (int base = 0; base < n; base += kEvThreads) {
-      const int i = base + t;
-      const uint32_t key = i < n ? evict_key(acc[i], i, p.sinks, tail) : 0u;
-      const bool in = i < n && (key & mask) == prefix;
-      const uint32_t digit = (key >> shift) & 255u;
-      const unsigned act = __ballot_sync(0xffffffffu, in);
-      if (in) {
-        const unsigned same = __match_any_sync(act, digit);
-        if (lane == __ffs(same) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(same));
-      }
-    }
-    __syncthreads();
-    if (t < 32) radix_pick(hist, need, &s_digit, &s_need);
-    __syncthreads();
-    prefix |= s_digit << shift;
-    mask |= 255u << shift;
-    need = s_need;
-    __syncthreads();
-  }
-  int written = 0, ties = 0;
-#pragma unroll 1
-  for (int base = 0; base < n; base += kEvThreads) {
-    const int i = base + t;
-    const float w = i < n ? acc[i] : 0.f;
-    const uint32_t key = i < n ? evict_key(w, i, p.sinks, tail) : 0u;
-    const bool gt = i < n && key > prefix, eq = i < n && key == prefix;
-    int eq_total, sel_total;
-    const int eq_rank = block_prefix_count(eq, sums, &eq_total);
-    const bool sel = gt || (eq && ties + eq_rank < need);
-    const int pos = block_prefix_count(sel, sums, &sel_total);
-    if (sel && written + pos < p.budget) {
-      kept[written + pos] = i;
-      out[written + pos] = w;
-    }
-    written += sel_total;
-    ties += eq_total;
-  }
-  __syncthreads();
-  for (int i = p.budget + t; i < n; i += kEvThreads) out[i] = 0.f;
-  if (t == 0) p.new_len[b] = p.budget;
 }
 
 // ------------------------------------------------------------ compaction
@@ -467,29 +416,23 @@ static smla_status run_select(const smla_evict_shape* s, const float* acc, const
                               int32_t* new_len, float* acc_out, cudaStream_t stream) {
   SelectParams p = {acc, ctx_len, kept, new_len, acc_out, s->max_ctx, s->budget, s->sinks, s->recent};
   void* args[] = {&p};
-  cudaError_t e;
-  if (s->max_ctx > kEvMaxCtas * kEvThreads * 16) {
-    e = launch_pdl((const void*)smla_evict_select_long_kernel, dim3((unsigned)s->batch), dim3(kEvThreads), 0, stream, args);
-  } else {
-    // eight weights per thread while the cluster's CTAs hold them all
-    const bool wide = s->max_ctx > kEvMaxCtas * kEvThreads * 8;
-    const int per = kEvThreads * (wide ? 16 : 8);
-    int ctas = 1;
-    while (ctas * per < s->max_ctx) ctas *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)s->batch);
-    cfg.blockDim = dim3(kEvThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)ctas;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = ctas > 1 ? 2 : 1;
-    e = cudaLaunchKernelExC(&cfg, wide ? (const void*)smla_evict_select_kernel<16> : (const void*)smla_evict_select_kernel<8>, args);
-  }
+  int ctas = 1;
+  while (ctas < kEvMaxCtas && ctas * kEvThreads * kEvPer < s->max_ctx) ctas *= 2;
+  const void* kern = ctas * kEvThreads * kEvPer < s->max_ctx ? (const void*)smla_evict_select_kernel<true>
+                                                             : (const void*)smla_evict_select_kernel<false>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)s->batch);
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, kern, args);
   return e == cudaSuccess ? SMLA_OK : SMLA_ERR_CUDA;
 }
 
