@@ -477,7 +477,8 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
   }
   if (k_cache) plane(k_cache, 64 * 256, 256, 16, s->num_key_rows);
   // In place a cluster per column: as many CTAs (a power of two, at most eight)
-  // as leave three to an SM.  New pages: a CTA per step.
+  // as leave three to an SM (one sequence of 65,536 -> 8,192 bf16 rows: 30 us
+  // with one CTA, 8 with eight).  New pages: a CTA per step.
   const int step_rows = (kCpThreads >> log2_lanes) * kCpBatch;
   p.ctas = 1;
   if (in_place) {
