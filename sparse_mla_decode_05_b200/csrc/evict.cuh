@@ -26,9 +26,11 @@ __device__ __forceinline__ uint32_t evict_key(float w, int i, int sinks, int tai
 
 // A cluster of CTAs per sequence, each thread holding eight weights of a tile of
 // ctas x 8,192 positions.  Radix select of the budget-th largest key by digits
-// of 11, 11 and 10 bits: each CTA counts its keys in shared memory, all read
-// the counts of all (distributed shared memory), and pick the same digit; it
-// ends as soon as all keys that start with the digits so far are kept.  Then
+// of 11, 11 and 10 bits: each CTA counts its keys in shared memory, adds its
+// counts that are not zero (a few hundred of 2,048) to every CTA's sums
+// (distributed shared memory; reading all counts of all CTAs instead took 4,100
+// cycles a digit), and all pick the same digit; it ends as soon as all keys
+// that start with the digits so far are kept.  Then
 // every key above the selection is kept and the lowest positions equal to it;
 // the CTAs exchange their counts to know where their kept positions go.
 // Contexts of one tile (65,536 positions with eight CTAs) read the weights
@@ -41,6 +43,9 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void red_cluster_u32(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void evict_sync(int ctas) {
   if (ctas > 1) cluster_sync_all();
@@ -74,8 +79,8 @@ __device__ __forceinline__ int prefix_counts(int* v) {
 
 template <bool kLong>     // more than one tile
 __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const SelectParams p) {
-  __shared__ uint32_t hist[2][2048];
-  __shared__ uint32_t total[2048];
+  __shared__ uint32_t hist[2048];
+  __shared__ uint32_t total[3][2048]; // by digit: the sums of all CTAs' counts
   __shared__ int cnt[32 * kEvPer];    // [k][warp] counts, then their prefix sums
   __shared__ int wsum[32];
   __shared__ int s_total[2][2];       // [tile parity]: this CTA's keys equal to the selection, and its kept keys
@@ -115,15 +120,18 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
     for (int k = 0; k < kEvPer; ++k) key[k] = evict_key(w[k], base + k * kEvThreads + t, p.sinks, tail);
   };
   load(0);
+  if (ctas > 1) {
+    for (int i = t; i < 3 * 2048; i += kEvThreads) total[0][i] = 0;
+    cluster_sync_all();               // all sums zero before any CTA adds to them
+  }
   uint32_t prefix = 0, mask = 0;
   int need = p.budget, eq_count = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
     const uint32_t dmask = pass == 2 ? 1023u : 2047u;
-    uint32_t* h = hist[pass & 1];
-    h[t] = 0;
-    h[t + 1024] = 0;
+    hist[t] = 0;
+    hist[t + 1024] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int first = 0; first < (kLong ? n : 1); first += tile) {
@@ -138,34 +146,23 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
         const unsigned zeros = __ballot_sync(0xffffffffu, zero), fixeds = __ballot_sync(0xffffffffu, fixed);
         if (zero || fixed) {
           const unsigned same = zero ? zeros : fixeds;
-          if (lane == __ffs(same) - 1) atomicAdd(&h[digit], (uint32_t)__popc(same));
+          if (lane == __ffs(same) - 1) atomicAdd(&hist[digit], (uint32_t)__popc(same));
         } else if (in) {
-          atomicAdd(&h[digit], 1u);
+          atomicAdd(&hist[digit], 1u);
         }
       }
     }
-    evict_sync(ctas);
+    __syncthreads();
     if (ctas > 1) {
-      // (all loads on their way before the first is used)
-      uint32_t x[kEvMaxCtas], y[kEvMaxCtas];
-      const uint32_t a = smem_u32(h + t);
 #pragma unroll
-      for (int r = 0; r < kEvMaxCtas; ++r) {
-        x[r] = y[r] = 0;
-        if (r < ctas) {
-          const uint32_t ra = mapa_shared(a, (uint32_t)r);
-          x[r] = ld_cluster_u32(ra);
-          y[r] = ld_cluster_u32(ra + 4096);
-        }
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t c = hist[t + 1024 * u], a = smem_u32(&total[pass][t + 1024 * u]);
+        if (c)
+          for (int r = 0; r < ctas; ++r) red_cluster_u32(mapa_shared(a, (uint32_t)r), c);
       }
-      uint32_t c0 = 0, c1 = 0;
-#pragma unroll
-      for (int r = 0; r < kEvMaxCtas; ++r) c0 += x[r], c1 += y[r];
-      total[t] = c0;
-      total[t + 1024] = c1;
-      __syncthreads();
+      cluster_sync_all();
     }
-    radix_pick2048(ctas > 1 ? total : h, need, wsum, &s_digit, &s_need, &s_cnt);
+    radix_pick2048(ctas > 1 ? total[pass] : hist, need, wsum, &s_digit, &s_need, &s_cnt);
     prefix |= s_digit << shift;
     mask |= dmask << shift;
     need = s_need;
