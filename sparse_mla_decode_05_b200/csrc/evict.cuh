@@ -291,8 +291,8 @@ template <> struct UnitOf<4> { using T = uint32_t; };
 // memory), so the moving threads wait for one memory latency a step and
 // spend few instructions on addresses.  Column widths, 32 x 4,096 fp8 rows and
 // keys: 64 / 128 bytes 52 / 53 us in place and 47 / 42 us into new pages; 32
-// bytes 67 / 65.  Bulk copies of whole rows through shared memory were twice
-// as slow.
+// bytes 67 / 65.  Bulk copies of whole rows through shared memory were two to
+// three times as slow.
 template <int kUnit, bool kInPlace>
 __device__ __forceinline__ void compact_column(const CompactParams& p, const EvictPlane& pl, const int* s_from, const int* s_to,
                                                int2 (*s_rows)[kCpMaxRows], volatile uint32_t* s_used, int column, int n) {
