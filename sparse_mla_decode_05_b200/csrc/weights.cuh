@@ -9,49 +9,57 @@ namespace smla {
 
 constexpr int kWtEpiWarps = 8;
 constexpr int kWtRing = 8;                         // tiles whose rows and scales are kept
-// Shared-memory operands are 128-byte-swizzled atoms of [rows][128 B]; the
-// last 64 bytes of a 576-byte fp8 row are a 64-byte-swizzled atom [rows][64 B].
+// Shared-memory operands are 128-byte-swizzled atoms of [rows][128 B].  Of a
+// 576-byte fp8 row the last 64 bytes, of a DeepSeek-V4 row's 448 codes the last
+// 64, are a 64-byte-swizzled atom [rows][64 B]; its 64 bf16 dims follow in an
+// atom of their own.
 template <int kKind>
 struct WtCfg {
-  static constexpr bool kFp8 = kKind == kKindFp8;
-  static constexpr int kQK = kKind == kKindDsv4 ? 512 : kDqk;
-  static constexpr int kRowBytes = kFp8 ? kQK : 2 * kQK;           // of an operand row
+  static constexpr bool kFp8 = kKind == kKindFp8, kDsv4 = kKind == kKindDsv4;
+  static constexpr bool kCodes = kFp8 || kDsv4;                    // multiplied as stored
+  static constexpr int kQK = kDsv4 ? 512 : kDqk;
+  static constexpr int kRowBytes = kCodes ? 576 : 2 * kQK;         // of an operand row
   // Entries per tile = MMA M.  The tensor cores take as long for 64 rows as
-  // for 128: fp8 rows, whose bytes arrive fastest per MMA, need the full rate
+  // for 128: rows of codes, whose bytes arrive fastest per MMA, need the full rate
   // (64 rows: 47.8 us on the batch of 128, the MMAs busy 63 % of it).
-  static constexpr int kM = kFp8 ? 128 : 64;
+  static constexpr int kM = kCodes ? 128 : 64;
   static constexpr int kAtom = kM * 128;                           // 128 bytes of each of the rows
   static constexpr int kStages = 2;
   static constexpr int kStageBytes = kM * kRowBytes;
-  static constexpr int kCopyWarps = kKind == kKindDsv4 ? 16 : 8;
+  static constexpr int kCopyWarps = 8;
   static constexpr int kRows = kM / kCopyWarps;                    // rows of a tile per copy warp
-  // fp8: eight warps more help the epilogue warps to stage the query.  Staged by
+  // Codes: eight warps more help the epilogue warps to stage the query.  Staged by
   // eight, a row's query took 10,000 cycles, longer than two stages of copies
   // last; by the copy warps too, it held up the copies.
-  static constexpr int kHelpers = kFp8 ? 8 : 0;
+  static constexpr int kHelpers = kCodes ? 8 : 0;
   static constexpr int kThreads = 32 * (1 + kWtEpiWarps + kCopyWarps + kHelpers);
   static constexpr int kQWarps = kWtEpiWarps + kHelpers;           // that stage the query
   static constexpr int kQHeads = kH / kQWarps;
   static constexpr int kQRows = kFp8 ? 128 : 64;                   // fp8: the heads' high parts, then their low parts
-  static constexpr int kQBytes = kQRows * kRowBytes;
+  static constexpr int kQPart = 64 * 448;                          // DeepSeek-V4: high parts, low parts, then the bf16 dims
+  static constexpr int kQBytes = kDsv4 ? 2 * kQPart + 64 * 128 : kQRows * kRowBytes;
   static constexpr int kMmaN = kQRows;
   // bf16 operands: the K steps go to four accumulators, added in the epilogue.
   // The tensor cores cut every update of an accumulator to fp32, an error in
   // proportion to its value and all of one sign; in a quarter each, partial
   // sums are a quarter as large (one sequence, scores up to 20: relative
   // error of the weights 7.7e-6 with one accumulator, 1.4e-6 with four; 1 % of
-  // the time).  DeepSeek-V4 rows, short of registers, take two; fp8 rows take
-  // half the steps, in two parts already.
-  static constexpr int kAccs = kFp8 ? 1 : (kKind == kKindBf16 ? 4 : 2);
+  // the time).  fp8 rows take half the steps, in two parts already.
+  // DeepSeek-V4 rows: one accumulator per scale group, whose scales the epilogue
+  // applies, and one for the bf16 dims: all of tensor memory, so one buffer.
+  static constexpr int kAccs = kFp8 ? 1 : (kDsv4 ? 8 : 4);
   static constexpr int kN = kAccs * kMmaN;                         // columns of a score buffer
-  static constexpr uint32_t kTmem = 2 * kN;
+  static constexpr int kBufs = kDsv4 ? 1 : 2;
+  static constexpr uint32_t kTmem = kBufs * kN;
   static constexpr int kSmemQ = kStages * kStageBytes;
   static constexpr int kSmemRow = kSmemQ + kQBytes;                // int  [kWtRing][kM] physical row or -1
-  static constexpr int kSmemScale = kSmemRow + kWtRing * kM * 4;   // f32  [kWtRing][kM] row scale (fp8)
-  static constexpr int kSmemLse = kSmemScale + kWtRing * kM * 4;   // f32  [2][64] by row parity
+  static constexpr int kSmemScale = kSmemRow + kWtRing * kM * 4;   // [kWtRing][kM] scales (codes)
+  static constexpr int kScaleBytes = kDsv4 ? 8 : 4;                // DeepSeek-V4: the row's block of scales
+  static constexpr int kSmemLse = kSmemScale + kWtRing * kM * kScaleBytes;   // f32  [2][64] by row parity
   static constexpr int kSmemK = kSmemLse + 2 * 64 * 4;             // f32  [2][64] scale, over the query's power of two
-  static constexpr int kSmemBar = kSmemK + 2 * 64 * 4;
-  static constexpr int kSmemTmem = kSmemBar + 8 * 16;
+  static constexpr int kSmemPart = kSmemK + 2 * 64 * 4;            // f32  [2][kM] sums of heads 32-63 (DeepSeek-V4), by tile parity
+  static constexpr int kSmemBar = kSmemPart + (kDsv4 ? 2 * kM * 4 : 0);
+  static constexpr int kSmemTmem = kSmemBar + 8 * 24;
   static constexpr int kSmemBytes = kSmemTmem + 16;
   static_assert(kSmemBytes <= 232448, "exceeds the 227 KB per-CTA shared memory of sm_100");
   static_assert(kSmemQ % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled operands need 1024-byte aligned atoms");
@@ -60,8 +68,9 @@ struct WtCfg {
   static_assert(kWtRing >= kStages + 2, "row ring");
 };
 constexpr uint32_t kIdescWt = make_idesc(64, 64, false, false), kIdescWt8 = make_idesc_e4m3(128, 128, false);
+constexpr uint32_t kIdescWtGroup = make_idesc_e4m3(128, 64, false), kIdescWtRope = make_idesc(128, 64, false, false);
 // barriers
-constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13, WB_ROW = 14;
+constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13, WB_ROW = 14, WB_PART = 16;
 
 // Shared-memory matrix descriptor, 64-byte swizzle (layout type 4), K-major:
 // rows of 64 B, 8-row groups 512 B apart.
@@ -74,6 +83,16 @@ template <int kRows>
 __device__ __forceinline__ uint32_t wt_off8(int r, int c) {
   return c < 32 ? (uint32_t)((c >> 3) * (kRows * 128)) + sw128_off(r, c & 7)
                 : (uint32_t)(4 * kRows * 128) + sw64_off(r, c - 32);
+}
+
+// and of a DeepSeek-V4 slot: 28 chunks of codes, then eight of bf16 dims
+template <int kRows>
+__device__ __forceinline__ uint32_t wt_off_codes(int r, int c) {
+  return c < 24 ? (uint32_t)((c >> 3) * (kRows * 128)) + sw128_off(r, c & 7) : (uint32_t)(3 * kRows * 128) + sw64_off(r, c - 24);
+}
+template <int kRows>
+__device__ __forceinline__ uint32_t wt_off_slot(int r, int c) {
+  return c < 28 ? wt_off_codes<kRows>(r, c) : (uint32_t)(448 * kRows) + sw128_off(r, c - 28);
 }
 
 struct WeightsParams {
@@ -134,13 +153,14 @@ __device__ __forceinline__ void split_e4m3x2_f16(uint32_t x, uint32_t& hi, uint3
 }
 
 // kHeads heads of a row's query (h0 ..) into the B operand, by one warp.
-// bf16 caches: as they are.  fp8: times the power of two that brings the
+// bf16 caches: as they are.  Codes: times the power of two that brings the
 // head's largest |q| into [128, 256), split into e4m3 high and low parts
 // (exact for the bf16 values whose parts are e4m3 normals, within 2^-10 of the
 // scaled value otherwise); s_k[h] receives scale over that power.  This runs
 // once per row between two rows' products, at a warp's own pace (a few cycles
 // an instruction), so it is spread over as many warps as there are and kept
-// short: bf16 pairs are scaled as pairs and split as f16 pairs.
+// short: bf16 pairs are scaled as pairs and split as f16 pairs.  (DeepSeek-V4's
+// last 64 dims are scaled alike and stay bf16.)
 template <int kKind, int kHeads>
 __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* smem, uint32_t sbase, int row, int h0,
                                                int lane, float* s_k) {
@@ -148,21 +168,22 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
   constexpr int kChunks = C::kQK / 8;               // 16-byte chunks of a head
   const uint8_t* q = p.q + ((size_t)row * kH + h0) * (C::kQK * 2);
   const uint32_t qb = sbase + C::kSmemQ;
-  if constexpr (!C::kFp8) {
+  if constexpr (!C::kCodes) {
     for (int c = lane; c < kHeads * kChunks; c += 32) {
       const int h = c / kChunks, j = c - h * kChunks;
       cp_async_16(qb + (uint32_t)((j >> 3) * (C::kQRows * 128)) + sw128_off(h0 + h, j & 7), q + (size_t)c * 16, 16u);
     }
     cp_async_wait_all();
   } else {
-    // lane l: chunks l, 32 + l and, of lanes 0-7, 64 + l
-    uint4 v[kHeads][3];
+    // lane l: chunks l, 32 + l and, where there are 72, of lanes 0-7, 64 + l
+    constexpr int kUnits = C::kDsv4 ? 2 : 3;
+    uint4 v[kHeads][kUnits];
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
       const uint4* src = reinterpret_cast<const uint4*>(q + (size_t)i * (C::kQK * 2));
       v[i][0] = __ldg(src + lane);
       v[i][1] = __ldg(src + 32 + lane);
-      v[i][2] = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kUnits == 3) v[i][2] = lane < 8 ? __ldg(src + 64 + lane) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -170,7 +191,7 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
       // largest magnitude (bf16 bits order as the magnitudes do)
       uint32_t m2 = 0;
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
+      for (int u = 0; u < kUnits; ++u) {
         m2 = __vmaxu2(m2, v[i][u].x & 0x7FFF7FFFu);
         m2 = __vmaxu2(m2, v[i][u].y & 0x7FFF7FFFu);
         m2 = __vmaxu2(m2, v[i][u].z & 0x7FFF7FFFu);
@@ -181,9 +202,14 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
       sq = sq > 120 ? 120 : (sq < -120 ? -120 : sq);
       const uint32_t up = (uint32_t)(127 + sq) * 0x00800080u;       // 2^sq as a bf16 pair
 #pragma unroll
-      for (int u = 0; u < 3; ++u) {
+      for (int u = 0; u < kUnits; ++u) {
         if (u == 2 && lane >= 8) continue;
         const uint32_t w4[4] = {v[i][u].x, v[i][u].y, v[i][u].z, v[i][u].w};
+        if (C::kDsv4 && u == 1 && lane >= 24) {
+          st_shared_v4(qb + 2 * C::kQPart + sw128_off(h, lane - 24),
+                       make_uint4(bf16x2_mul(w4[0], up), bf16x2_mul(w4[1], up), bf16x2_mul(w4[2], up), bf16x2_mul(w4[3], up)));
+          continue;
+        }
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -193,10 +219,16 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
         // eight codes: half of 16-byte chunk (32 u + lane) / 2 of the row
         const int c = (32 * u + lane) >> 1;
         const uint32_t at = (uint32_t)(8 * (lane & 1));
-        *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(h, c) + at) =
-            make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-        *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(64 + h, c) + at) =
-            make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        if constexpr (C::kDsv4) {
+          uint8_t* dst = smem + C::kSmemQ + wt_off_codes<64>(h, c) + at;
+          *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(dst + C::kQPart) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        } else {
+          *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(h, c) + at) =
+              make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(smem + C::kSmemQ + wt_off8<C::kQRows>(64 + h, c) + at) =
+              make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        }
       }
       if (lane == 0) s_k[h] = p.scale * pow2i(-sq);
     }
@@ -206,7 +238,7 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
 // The decode rows' tiles are laid end to end and shared out
 // evenly over one CTA per SM; every tile's weights are its own, so nothing is
 // merged.  Warp roles: one MMA issuer; eight epilogue warps, which also
-// stage the query of each row the CTA meets (for fp8 rows with eight more);
+// stage the query of each row the CTA meets (for codes with eight more);
 // the copy warps.
 //  * Copy warps resolve and gather kRows rows each of every tile by 16-byte
 //    cp.async (lane = chunk of one row, the rows' last 64 bytes merged):
@@ -214,14 +246,19 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
 //  * S[entries x 64 heads] = K Q^T in tensor memory, two buffers.  fp8 rows
 //    are multiplied as stored (kind::f8f6f4) by the query scaled per head by
 //    a power of two and split into e4m3 high and low parts, as in the decode:
-//    columns 0-63 and 64-127 of the buffer.
+//    columns 0-63 and 64-127 of the buffer.  DeepSeek-V4 codes too, each group
+//    of 64 dims into 64 columns of its own, high and low parts added there
+//    (converting the codes to bf16 instead took 14,400 instructions per 64
+//    entries, 79 us on 128 x 2,048 entries against 40 now, for a relative
+//    error of 1.1e-7 against 1.3e-7, the query's split).
 //  * Epilogue warps 0-3 take the even tiles, 4-7 the odd ones; a thread has one
 //    entry: of 128-entry tiles all heads, of 64-entry tiles 32, the other 32
-//    being its partner's, sixteen lanes on.
+//    being its partner's, sixteen lanes on.  DeepSeek-V4 (one buffer): all eight
+//    take every tile, warps 4-7 heads 32-63, and hand their sums to warps 0-3.
 template <int kKind>
 __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel(const __grid_constant__ WeightsParams p) {
   using C = WtCfg<kKind>;
-  constexpr bool kFp8 = C::kFp8, kDsv4 = kKind == kKindDsv4;
+  constexpr bool kFp8 = C::kFp8, kDsv4 = C::kDsv4;
   constexpr int kStages = C::kStages, kM = C::kM, kRows = C::kRows, kAtom = C::kAtom;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -239,17 +276,18 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
   const int row0 = (int)(g0 / nt), tin0 = (int)(g0 % nt);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      // a copying thread's copies (fp8, bf16), and each copy warp's row numbers or converted rows
-      mbar_init(BAR(WB_FULL + i), C::kCopyWarps + (kDsv4 ? 0 : 32 * C::kCopyWarps));
+      // a copying thread's copies, and each copy warp's row numbers
+      mbar_init(BAR(WB_FULL + i), 33 * C::kCopyWarps);
       mbar_init(BAR(WB_EMPTY + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(BAR(WB_SF + i), 1);
-      mbar_init(BAR(WB_SE + i), kWtEpiWarps / 2);
+      mbar_init(BAR(WB_SE + i), kWtEpiWarps / C::kBufs);
     }
     mbar_init(BAR(WB_Q), C::kQWarps);
     mbar_init(BAR(WB_FIN), 1);
     mbar_init(BAR(WB_ROW), 1);
+    for (int i = 0; i < 8; ++i) mbar_init(BAR(WB_PART + i), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -275,9 +313,9 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
     bool ok = true;
     int tin = tin0, seg = 0;
     for (int t = 0; ok && t < count; ++t, tin = tin + 1 == nt ? 0 : tin + 1) {
-      const int stage = t % kStages, buf = t & 1;
+      const int stage = t % kStages, buf = t % C::kBufs;
       if (t == 0 || tin == 0) ok = wait_all(WB_Q, seg++ & 1);
-      if (ok && t >= 2) ok = wait_all(WB_SE + buf, ((t >> 1) - 1) & 1);
+      if (ok && t >= C::kBufs) ok = wait_all(WB_SE + buf, (t / C::kBufs - 1) & 1);
       if (ok) ok = wait_all(WB_FULL + stage, (t / kStages) & 1);
       if (!ok) break;
       tc_fence_after();
@@ -294,6 +332,24 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
         const uint64_t ta = sw64_desc(a + 4 * kAtom), tb = sw64_desc(b + 4 * C::kQRows * 128);
 #pragma unroll
         for (int k = 0; k < 2; ++k) mma8_ss_elect(d, ta + (uint64_t)(2 * k), tb + (uint64_t)(2 * k), idesc, true);
+      } else if constexpr (kDsv4) {
+#pragma unroll
+        for (int g = 0; g < 7; ++g) {
+          const uint32_t dg = d + (uint32_t)(64 * g);
+          // the group's 64 bytes of a row: half an atom, or the 64-byte one
+          const uint64_t da = g < 6 ? sw128_desc(a + (g >> 1) * kAtom, 16, 1024) + (uint64_t)((g & 1) * 4) : sw64_desc(a + 3 * kAtom);
+          const uint32_t bg = b + (g < 6 ? (g >> 1) : 3) * 8192;
+          const uint64_t dh = g < 6 ? sw128_desc(bg, 16, 1024) + (uint64_t)((g & 1) * 4) : sw64_desc(bg);
+          const uint64_t dl = dh + (uint64_t)(C::kQPart >> 4);
+          mma8_ss_elect(dg, da, dh, kIdescWtGroup, false);
+          mma8_ss_elect(dg, da + 2, dh + 2, kIdescWtGroup, true);
+          mma8_ss_elect(dg, da, dl, kIdescWtGroup, true);
+          mma8_ss_elect(dg, da + 2, dl + 2, kIdescWtGroup, true);
+        }
+        const uint64_t ra = sw128_desc(a + 448 * kM, 16, 1024), rb = sw128_desc(b + 2 * C::kQPart, 16, 1024);
+        mma_set_elect(d + 448u, ra, rb, kIdescWtRope);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) mma_acc_elect(d + 448u, ra + (uint64_t)(2 * k), rb + (uint64_t)(2 * k), kIdescWtRope);
       } else {
         const uint32_t idesc = kIdescWt;
         const uint64_t da = sw128_desc(a, 16, 1024), db = sw128_desc(b, 16, 1024);
@@ -333,7 +389,7 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
           // a head without any valid entry has lse -inf and takes no part
           const float l = __ldg(p.lse + (size_t)row * kH + h0 + lane);
           s_lse[sb + h0 + lane] = l == -INFINITY ? INFINITY : l;
-          if (!kFp8) s_k[sb + h0 + lane] = p.scale;
+          if (!C::kCodes) s_k[sb + h0 + lane] = p.scale;
         }
         wt_stage_query<kKind, C::kQHeads>(p, smem, sbase, row, C::kQHeads * ew, lane, s_k + sb);
         fence_proxy_async_smem();
@@ -341,16 +397,18 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
         if (lane == 0) mbar_arrive(BAR(WB_Q));
         ++seg;
       }
-      if ((t & 1) == group) {
-        ok = wait_all(WB_SF + group, (t >> 1) & 1);
+      if (C::kBufs == 1 || (t & 1) == group) {
+        const int buf = C::kBufs == 1 ? 0 : group;
+        ok = wait_all(WB_SF + buf, (t / C::kBufs) & 1);
         if (!ok) break;
         tc_fence_after();
         const int rs = (t % kWtRing) * kM + e;
         const int r = s_row[rs];
         const float rsc = kFp8 ? s_scale[rs] : 1.f;
-        const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(group * C::kN);
-        const float* lse = s_lse + ((seg - 1) & 1) * 64 + 32 * half;
-        const float* kh = s_k + ((seg - 1) & 1) * 64 + 32 * half;
+        const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + (uint32_t)(buf * C::kN);
+        const int hp = kDsv4 ? group : half;                     // which 32 heads
+        const float* lse = s_lse + ((seg - 1) & 1) * 64 + 32 * hp;
+        const float* kh = s_k + ((seg - 1) & 1) * 64 + 32 * hp;
         // scale q.k - lse in natural units and one rounding: where a weight is
         // large the difference is small, so the exponential is taken of a
         // number known to its own last bits, not to those of the lse
@@ -367,7 +425,7 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
         auto taken = [&]() {      // the score buffer has been read
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(WB_SE + group));
+          if (lane == 0) mbar_arrive(BAR(WB_SE + buf));
         };
         float sum = 0.f;
         if constexpr (kFp8) {
@@ -382,6 +440,51 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
 #pragma unroll
             for (int h = 0; h < 16; ++h) x[h] += lo[h];
             sum += weigh(x, lse + 16 * g, kh + 16 * g);
+          }
+        } else if constexpr (kDsv4) {
+          // the entry's scales: bytes 2^(e - 127), e = 0 a subnormal
+          const uint2 sc = *reinterpret_cast<const uint2*>(smem + C::kSmemScale + rs * 8);
+          auto group_scale = [&](int g) -> float {
+            const uint32_t ex = ((g < 4 ? sc.x : sc.y) >> (8 * (g & 3))) & 0xFFu;
+            return __uint_as_float(ex ? ex << 23 : 0x00400000u);
+          };
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float x[16], y[16], z[16];
+            const uint32_t dh = d + (uint32_t)(32 * group + 16 * hh);
+            tmem_ld_32x32b_x16(dh + 448u, x);              // the bf16 dims
+            tmem_ld_32x32b_x16(dh, y);
+            tmem_wait_ld();
+            const float s0 = group_scale(0);
+#pragma unroll
+            for (int h = 0; h < 16; ++h) x[h] = fmaf(y[h], s0, x[h]);
+#pragma unroll
+            for (int g = 1; g < 7; g += 2) {
+              tmem_ld_32x32b_x16(dh + 64u * (uint32_t)g, y);
+              tmem_ld_32x32b_x16(dh + 64u * (uint32_t)(g + 1), z);
+              tmem_wait_ld();
+              if (hh == 1 && g == 5) taken();
+              const float sy = group_scale(g), sz = group_scale(g + 1);
+#pragma unroll
+              for (int h = 0; h < 16; ++h) x[h] = fmaf(z[h], sz, fmaf(y[h], sy, x[h]));
+            }
+            sum += weigh(x, lse + 16 * hh, kh + 16 * hh);
+          }
+          // One sum per entry: warps 4-7 hand theirs to warps 0-3, by slots and
+          // barriers of the tile's parity.  Both are free again at tile t: its
+          // products waited for warps 0-3 to let go of tile t - 1's, after they had
+          // ended tile t - 2.  (By one barrier, warps 4-7 could complete tile t + 1's
+          // phase while warps 0-3, who let go of the products before they wait
+          // here, had not yet seen tile t's.)
+          float* part = reinterpret_cast<float*>(smem + C::kSmemPart) + (t & 1) * kM + e;
+          if (group == 1) {
+            *part = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(BAR(WB_PART + 4 * (t & 1) + quarter));
+          } else {
+            ok = wait_all(WB_PART + 4 * (t & 1) + quarter, (t >> 1) & 1);
+            if (!ok) break;
+            sum += *part;
           }
         } else {
 #pragma unroll
@@ -401,7 +504,7 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         }
         const int at = tin * kM + e;
-        if (half == 0 && at < p.topk) p.out[(size_t)row * p.topk + at] = r >= 0 ? sum : 0.f;
+        if (half == 0 && (!kDsv4 || group == 0) && at < p.topk) p.out[(size_t)row * p.topk + at] = r >= 0 ? sum : 0.f;
       }
       if (++tin == nt) {
         tin = 0;
@@ -434,115 +537,71 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
       const int at = c.tin * kM + first + (lane & (kRows - 1));
       return t < count && at < p.topk ? __ldg(p.indices + (size_t)c.row * p.topk + at) : -1;
     };
-    // DeepSeek-V4: a tile's part in registers.  Lane l has chunk l (16 codes, or
-    // from chunk 28 on eight bf16 dims) of each of the warp's rows and the scale
-    // of its 64 dims; lanes 0 - 15 also one of the rows' last four chunks.
-    uint4 va[kRows + 1], vb[kRows + 1];
-    uint32_t sa[kRows], sb[kRows];
-    auto dsv4_load = [&](int rows, uint4 (&v)[kRows + 1], uint32_t (&sc)[kRows]) {
-#pragma unroll
-      for (int u = 0; u <= kRows; ++u) {
-        const int r = __shfl_sync(0xffffffffu, rows, u < kRows ? u : (lane >> 2) & (kRows - 1));
-        v[u] = make_uint4(0u, 0u, 0u, 0u);
-        if (u < kRows) sc[u] = 127u;
-        if (r < 0 || (u == kRows && lane >= 4 * kRows)) continue;
-        const uint8_t* page = p.kv + (size_t)(r >> 6) * kDsv4Page;
-        v[u] = __ldg(reinterpret_cast<const uint4*>(page + (r & 63) * kDsv4Slot + 16 * (u < kRows ? lane : 32 + (lane & 3))));
-        if (u < kRows && lane < 28) sc[u] = __ldg(page + kDsv4ScaleOff + (r & 63) * 8 + (lane >> 2));
-      }
-    };
     const int i0 = entry(c2, 0);
     c2 = next(c2);
     const int i1 = entry(c2, 1);
     int r0 = resolve_row(p, i0, row0), r1 = resolve_row(p, i1, c2.row);
     c2 = next(c2);
     int i2 = entry(c2, 2);
-    // one tile: true unless a wait gave up.  (DeepSeek-V4: stores `now`, loads the
-    // next tile's part into `then`; the two swap from tile to tile, as moving
-    // registers would wait for the loads.)
-    auto copy_tile = [&](int t, uint4 (&now)[kRows + 1], uint32_t (&snow)[kRows], uint4 (&then)[kRows + 1],
-                         uint32_t (&sthen)[kRows]) -> bool {
+    for (int t = 0; t < count; ++t) {
       const int stage = t % kStages, rs = (t % kWtRing) * kM;
       const int r2 = resolve_row(p, i2, c2.row);
       c2 = next(c2);
       i2 = entry(c2, t + 3);
       const uint32_t base = sbase + (uint32_t)(stage * C::kStageBytes);
-      if constexpr (kDsv4) {
-        // codes to bf16 on the way
-        dsv4_load(r1, then, sthen);
-        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) return false;
-        const int g = lane >> 2;
+      if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) break;
+      // one instruction per row and 512 bytes, then the rows' tails
+      // together.  Absent rows read nothing and are zero.
+      auto row_at = [&](int r) -> const uint8_t* {
+        const uint32_t at = (uint32_t)(r >= 0 ? r : 0);
+        if constexpr (kDsv4) return p.kv + (size_t)(at >> 6) * kDsv4Page + (at & 63u) * kDsv4Slot;
+        else return p.kv + (size_t)at * C::kRowBytes;
+      };
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          const int tok = first + u;
-          if (lane < 28) {
-            const uint32_t s2 = ue8m0_bf16x2(snow[u]);
-            uint4 lo, hi;
-            e4m3x4_to_bf16x4_scaled(now[u].x, s2, lo.x, lo.y);
-            e4m3x4_to_bf16x4_scaled(now[u].y, s2, lo.z, lo.w);
-            e4m3x4_to_bf16x4_scaled(now[u].z, s2, hi.x, hi.y);
-            e4m3x4_to_bf16x4_scaled(now[u].w, s2, hi.z, hi.w);
-            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (lane & 3)), lo);
-            st_shared_v4(base + g * kAtom + sw128_off(tok, 2 * (lane & 3) + 1), hi);
-          } else {
-            st_shared_v4(base + 7 * kAtom + sw128_off(tok, lane - 28), now[u]);
-          }
-        }
-        if (lane < 4 * kRows) st_shared_v4(base + 7 * kAtom + sw128_off(first + g, 4 + (lane & 3)), now[kRows]);
-        if (lane < kRows) s_row[rs + first + lane] = r0;
-        fence_proxy_async_smem();
-      } else {
-        if (t >= kStages && !wait_all(WB_EMPTY + stage, ((t / kStages) - 1) & 1)) return false;
-        // one instruction per row and 512 bytes, then the rows' tails
-        // together.  Absent rows read nothing and are zero.
-#pragma unroll
-        for (int rr = 0; rr < kRows; ++rr) {
-          const int r = __shfl_sync(0xffffffffu, r0, rr);
-          const uint32_t n = r >= 0 ? 16u : 0u;
-          const uint8_t* src = p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + lane * 16;
-          if constexpr (kFp8) {
-            cp_async_16(base + wt_off8<kM>(first + rr, lane), src, n);
-          } else {
-            const uint32_t at = base + (uint32_t)((lane >> 3) * kAtom) + sw128_off(first + rr, lane & 7);
-            cp_async_16(at, src, n);
-            cp_async_16(at + 4 * kAtom, src + 512, n);
-          }
-        }
+      for (int rr = 0; rr < kRows; ++rr) {
+        const int r = __shfl_sync(0xffffffffu, r0, rr);
+        const uint32_t n = r >= 0 ? 16u : 0u;
+        const uint8_t* src = row_at(r) + lane * 16;
         if constexpr (kFp8) {
-#pragma unroll
-          for (int hh = 0; hh < kRows / 8; ++hh) {
-            const int rr = 8 * hh + (lane >> 2), r = __shfl_sync(0xffffffffu, r0, rr);
-            cp_async_16(base + wt_off8<kM>(first + rr, 32 + (lane & 3)),
-                        p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 512 + (lane & 3) * 16, r >= 0 ? 16u : 0u);
-          }
-          // the row's scale rides along (a copy of four bytes)
-          if (lane < kRows)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(s_scale + rs + first + lane)),
-                         "l"(p.kv_row_scale + (r0 >= 0 ? r0 : 0)) : "memory");
+          cp_async_16(base + wt_off8<kM>(first + rr, lane), src, n);
+        } else if constexpr (kDsv4) {
+          cp_async_16(base + wt_off_slot<kM>(first + rr, lane), src, n);
         } else {
-#pragma unroll
-          for (int hh = 0; hh < kRows / 4; ++hh) {
-            const int rr = 4 * hh + (lane >> 3), r = __shfl_sync(0xffffffffu, r0, rr);
-            cp_async_16(base + 8 * kAtom + sw128_off(first + rr, lane & 7),
-                        p.kv + (size_t)(r >= 0 ? r : 0) * C::kRowBytes + 1024 + (lane & 7) * 16, r >= 0 ? 16u : 0u);
-          }
+          const uint32_t at = base + (uint32_t)((lane >> 3) * kAtom) + sw128_off(first + rr, lane & 7);
+          cp_async_16(at, src, n);
+          cp_async_16(at + 4 * kAtom, src + 512, n);
         }
-        if (lane < kRows) s_row[rs + first + lane] = r0;
-        cp_async_mbar_arrive_noinc(BAR(WB_FULL + stage));
       }
+      if constexpr (C::kCodes) {
+#pragma unroll
+        for (int hh = 0; hh < kRows / 8; ++hh) {
+          const int rr = 8 * hh + (lane >> 2), r = __shfl_sync(0xffffffffu, r0, rr), c = 32 + (lane & 3);
+          cp_async_16(base + (kDsv4 ? wt_off_slot<kM>(first + rr, c) : wt_off8<kM>(first + rr, c)), row_at(r) + c * 16,
+                      r >= 0 ? 16u : 0u);
+        }
+        // the row's scales ride along (a copy of four or eight bytes)
+        if (lane < kRows) {
+          const uint32_t dst = sbase + (uint32_t)(C::kSmemScale + (rs + first + lane) * C::kScaleBytes);
+          const uint32_t at = (uint32_t)(r0 >= 0 ? r0 : 0);
+          if constexpr (kDsv4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst),
+                         "l"(p.kv + (size_t)(at >> 6) * kDsv4Page + kDsv4ScaleOff + (at & 63u) * 8) : "memory");
+          else
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(p.kv_row_scale + at) : "memory");
+        }
+      } else {
+#pragma unroll
+        for (int hh = 0; hh < kRows / 4; ++hh) {
+          const int rr = 4 * hh + (lane >> 3), r = __shfl_sync(0xffffffffu, r0, rr);
+          cp_async_16(base + 8 * kAtom + sw128_off(first + rr, lane & 7), row_at(r) + 1024 + (lane & 7) * 16, r >= 0 ? 16u : 0u);
+        }
+      }
+      if (lane < kRows) s_row[rs + first + lane] = r0;
+      cp_async_mbar_arrive_noinc(BAR(WB_FULL + stage));
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR(WB_FULL + stage));
       r0 = r1;
       r1 = r2;
-      return true;
-    };
-    if constexpr (kDsv4) {
-      dsv4_load(r0, va, sa);
-      for (int t = 0; t < count; t += 2)
-        if (!copy_tile(t, va, sa, vb, sb) || (t + 1 < count && !copy_tile(t + 1, vb, sb, va, sa))) break;
-    } else {
-      for (int t = 0; t < count; ++t)
-        if (!copy_tile(t, va, sa, vb, sb)) break;
     }
     cp_async_wait_all();
   }
