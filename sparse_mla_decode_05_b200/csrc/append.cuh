@@ -170,18 +170,14 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       wb = __ldg(p.norm_weight + db);
     }
   }
-  for (int j = 0; j < count; ++j) {
+  int j = 0;
+  for (; j < count; ++j) {
     const long long row = __shfl_sync(0xffffffffu, place, j);
     const int pos = __shfl_sync(0xffffffffu, position, j);
     const T* x = xs + j * p.x_stride;
     if constexpr (kVec) {
       const int st = j % kApStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar + 8u * (uint32_t)st, (uint32_t)((j / kApStages) & 1)))) {
-        // given up: the rows under way land before the shared memory is left
-        for (int k = j; k < min(count, j + kApStages); ++k)
-          mbar_wait(bar + 8u * (uint32_t)(k % kApStages), (uint32_t)((k / kApStages) & 1));
-        return;
-      }
+      if (!__all_sync(0xffffffffu, mbar_wait(bar + 8u * (uint32_t)st, (uint32_t)((j / kApStages) & 1)))) break;
       x = reinterpret_cast<const T*>(s_x + (warp * kApStages + st) * kRowB);
     }
     const RopeVec<T, 8> x0 = ap_load8<T, kVec>(x + 8 * lane), x1 = ap_load8<T, kVec>(x + 256 + 8 * lane);
@@ -322,6 +318,11 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       if (lane == 0) *reinterpret_cast<uint2*>(page + kDsv4ScaleOff + (row & 63) * 8) = block;
     }
   }
+  // a wait gave up: the rows under way land (or run out of time too) before the
+  // shared memory is left
+  if (kVec)
+    for (int k = j; k < min(count, j + kApStages); ++k)
+      mbar_wait(bar + 8u * (uint32_t)(k % kApStages), (uint32_t)((k / kApStages) & 1));
 }
 
 // ------------------------------------------------------------------ host
