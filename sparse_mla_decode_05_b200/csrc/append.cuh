@@ -73,6 +73,10 @@ __device__ __forceinline__ float ap_rcp(float x) {     // within one ulp
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// x (not negative) in [2^-96, 2^96): two integer instructions
+__device__ __forceinline__ bool ap_ordinary(float x) {
+  return __float_as_uint(x) - (31u << 23) < (192u << 23);
+}
 // eight fp32 -> eight e4m3 codes
 __device__ __forceinline__ uint2 ap_codes8(const float (&v)[8]) {
   return make_uint2(pack_e4m3x2(v[0], v[1]) | (pack_e4m3x2(v[2], v[3]) << 16),
@@ -256,13 +260,19 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
         return fmaf(fmaf(-q, scale, x), inv, q);
       };
       if (p.norm_weight) {
-        float rinv = r * inv;
-        if (latent * r >= rope && scale > 1.1754943508222875e-38f && m > 0.f) {
+        // (One factor only while it is an ordinary number: rows of tiny values
+        // would make it infinite, and 0 times infinity a NaN.)
+        float f = r * inv;
+        if (latent * r >= rope && scale > 1.1754943508222875e-38f && ap_ordinary(latent)) {
           const float y = ap_rcp(latent);
-          rinv = 448.0f * fmaf(fmaf(-latent, y, 1.0f), y, y);
+          f = 448.0f * fmaf(fmaf(-latent, y, 1.0f), y, y);
+        } else if (!ap_ordinary(f)) {
+          ap_scale8(v0, r);
+          ap_scale8(v1, r);
+          f = inv;
         }
-        ap_scale8(v0, rinv);
-        ap_scale8(v1, rinv);
+        ap_scale8(v0, f);
+        ap_scale8(v1, f);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
