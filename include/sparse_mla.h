@@ -545,7 +545,9 @@ typedef struct {
  * A slot, sequence or page outside its range writes nothing and sets bit 2
  * of the device error word.  Two tokens of one call may not name the same
  * row (it would hold parts of both).  Rows that no token names keep their
- * bytes.  Values are expected finite. */
+ * bytes.  Values are expected finite, and with norm_weight the mean square and
+ * 1 / sqrt(mean square + eps) are expected in fp32's range: values up to 2^63,
+ * and no row of zeros, or of values below 2^-62 alone, where eps is 0. */
 smla_status sparse_mla_cache_append(const smla_append_shape* shape, const void* x, const float* norm_weight,
                                     const smla_rope_table* table, const int32_t* positions, const int32_t* slots,
                                     const int32_t* seq, const int32_t* page_table, void* kv_cache,
