@@ -584,10 +584,10 @@ smla_status sparse_mla_attn_weights(const smla_shape* shape, const void* q, cons
  *             that got nothing are then not written)
  *   acc       [batch, max_ctx] fp32, updated
  * The sum of a position is taken in 64-bit fixed point whose unit is at most
- * 2^-62 of (entries, rounded up to a power of two) * twice the sequence's
- * largest |weight|, so it does not depend on the order of the entries; it is
- * added in fp64 and rounded once.  A NaN or infinite weight makes its
- * position NaN. */
+ * 2^-62 of (entries, rounded up to a power of two) * twice the position's
+ * largest |weight|, so it does not depend on the order of the entries, nor on
+ * what other positions got; it is added in fp64 and rounded once.  A NaN or
+ * infinite weight makes its position NaN. */
 smla_status sparse_mla_accumulate_weights(int32_t batch, int64_t entries, int32_t max_ctx, const int32_t* indices,
                                           const float* weights, float decay, float* acc, void* stream);
 

@@ -614,13 +614,17 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
 // One CTA per (sequence, range of kRange positions).  The entries of the
 // sequence that fall into the range are summed in 64-bit fixed point in
 // shared memory: integer addition is associative, so the result does not
-// depend on the order of the atomics, whatever positions repeat.  The unit is
-// 2^-s for all ranges of a sequence, s as large as keeps (entries x largest
-// |weight|) below 2^62: sums keep at least 46 bits below the largest weight.
+// depend on the order of the atomics, whatever positions repeat.  Each position
+// has a unit of its own, 2^-s, s as large as keeps (entries x its largest
+// |weight|) below 2^62: a sum keeps 61 - log2(entries, rounded up to a power of
+// two) bits below that weight (49 of 4,096 entries, 33 of 2^28), whatever weight
+// other positions got (with one unit for a whole sequence, 5e-14 beside a 64 was lost).
+// So the range's entries are gone through twice, for the largest weights and
+// for the sums.
 // Every CTA reads the sequence's whole list (from L2 after the first); what
 // bounds a call is its chain of latencies, so the list's first kAcKeep entries
 // per thread and the range's old sums are all loaded at the start (batch 16 x
-// 512 entries: 4.7 us with the loads where they are used, 2.3 now).
+// 512 entries: 4.7 us with the loads where they are used, 2.3 so).
 constexpr int kAcThreads = 512;
 constexpr int kAcKeep = 8;             // entries per thread held in registers
 
@@ -636,9 +640,9 @@ struct AccumulateParams {
 template <int kRange>
 __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const AccumulateParams p) {
   constexpr int kPos = kRange / kAcThreads;
-  __shared__ long long sum[kRange];
+  __shared__ long long sum[kRange];         // first the largest |weight| (its bits), then the sum
+  __shared__ uint8_t top[kRange];           // exponent field of the largest |weight|
   __shared__ uint32_t bad[kRange / 32];     // positions that got a NaN or an infinity
-  __shared__ int s_max;
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x, b = blockIdx.y, p0 = blockIdx.x * kRange;
@@ -659,48 +663,53 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
 #pragma unroll
   for (int j = 0; j < kPos; ++j) sum[j * kAcThreads + t] = 0;
   if (t < kRange / 32) bad[t] = 0;
-  if (t == 0) s_max = 0;
   __syncthreads();
-  // largest finite |weight| (as bits) of the sequence's entries; at least the
-  // smallest number where any entry is NaN or infinite
-  int m = 0;
-  bool outside = false;
-  auto look = [&](int pos, float v) {
-    const int bits = __float_as_int(fabsf(v));
-    outside |= pos >= p.max_ctx;
-    if (pos >= 0 && pos < p.max_ctx) m = max(m, bits < 0x7F800000 ? bits : 1);
-  };
-#pragma unroll
-  for (int j = 0; j < kAcKeep; ++j) look(at[j], wt[j]);
-  for (int i = kAcKeep * kAcThreads + t; i < p.entries; i += kAcThreads) look(__ldg(idx + i), __ldg(w + i));
-  m = __reduce_max_sync(0xffffffffu, m);
-  if ((t & 31) == 0 && m > 0) atomicMax(&s_max, m);
-  if (outside && p0 == 0) atomicOr(&g_error_word, 4u);
-  __syncthreads();
-  m = s_max;
-  if (m == 0 && p.decay == 1.0f) return;
-  // largest < 2^(e + 1): the unit's exponent
-  const int e = m >= 0x800000 ? (m >> 23) - 127 : -126;
-  const int s = 62 - p.log2_entries - (e + 1);
-  auto power = [](int k) -> double { return __longlong_as_double((long long)(1023 + k) << 52); };
-  const double up = power(s), down = power(-s);
-  auto add = [&](int pos, float v) {
-    if (pos < p0 || pos - p0 >= here) return;
-    pos -= p0;
-    if (fabsf(v) < INFINITY) {
-      // 64 bits as two native 32-bit additions with the carry between them
-      const unsigned long long x = (unsigned long long)__double2ll_rn((double)v * up);
-      uint32_t* at2 = reinterpret_cast<uint32_t*>(&sum[pos]);
-      const uint32_t before = atomicAdd(at2, (uint32_t)x);
-      const uint32_t high = (uint32_t)(x >> 32) + (before + (uint32_t)x < before ? 1u : 0u);
-      if (high) atomicAdd(at2 + 1, high);
-    } else {
-      atomicOr(&bad[pos >> 5], 1u << (pos & 31));
+  bool any = false, outside = false;
+  // place of an entry in the range; -1: it takes no part in the sums
+  auto look = [&](int entry, float v) -> int {
+    outside |= entry >= p.max_ctx;
+    const uint32_t pos = (uint32_t)entry - (uint32_t)p0, bits = __float_as_uint(fabsf(v));
+    if (pos >= (uint32_t)here || bits == 0) return -1;
+    any = true;
+    if (bits < 0x7F800000u) {
+      atomicMax(reinterpret_cast<uint32_t*>(&sum[pos]), bits);
+      return (int)pos;
     }
+    atomicOr(&bad[pos >> 5], 1u << (pos & 31));
+    return -1;
   };
 #pragma unroll
-  for (int j = 0; j < kAcKeep; ++j) add(at[j], wt[j]);
-  for (int i = kAcKeep * kAcThreads + t; i < p.entries; i += kAcThreads) add(__ldg(idx + i), __ldg(w + i));
+  for (int j = 0; j < kAcKeep; ++j) at[j] = look(at[j], wt[j]);
+  for (int i = kAcKeep * kAcThreads + t; i < p.entries; i += kAcThreads) look(__ldg(idx + i), __ldg(w + i));
+  if (outside && p0 == 0) atomicOr(&g_error_word, 4u);
+  if (!__syncthreads_or(any) && p.decay == 1.0f) return;
+#pragma unroll
+  for (int j = 0; j < kPos; ++j) {
+    const int i = j * kAcThreads + t;
+    const uint32_t field = (uint32_t)sum[i] >> 23;
+    top[i] = (uint8_t)(field ? field : 1u);          // (subnormal weights: the smallest normal one's)
+    sum[i] = 0;
+  }
+  __syncthreads();
+  // the largest weight of exponent field f is below 2^(f - 126)
+  const int s0 = 62 - p.log2_entries + 126;
+  auto power = [](int k) -> double { return __hiloint2double((1023 + k) << 20, 0); };
+  auto add = [&](int pos, float v) {
+    // 64 bits as two native 32-bit additions with the carry between them
+    const unsigned long long x = (unsigned long long)__double2ll_rn((double)v * power(s0 - top[pos]));
+    uint32_t* at2 = reinterpret_cast<uint32_t*>(&sum[pos]);
+    const uint32_t before = atomicAdd(at2, (uint32_t)x);
+    const uint32_t high = (uint32_t)(x >> 32) + (before + (uint32_t)x < before ? 1u : 0u);
+    if (high) atomicAdd(at2 + 1, high);
+  };
+#pragma unroll
+  for (int j = 0; j < kAcKeep; ++j)
+    if (at[j] >= 0) add(at[j], wt[j]);
+  for (int i = kAcKeep * kAcThreads + t; i < p.entries; i += kAcThreads) {
+    const uint32_t pos = (uint32_t)__ldg(idx + i) - (uint32_t)p0;
+    const float v = __ldg(w + i);
+    if (pos < (uint32_t)here && fabsf(v) < INFINITY) add((int)pos, v);
+  }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < kPos; ++j) {
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
     const long long v = sum[i];
     const bool nan = (bad[i >> 5] >> (i & 31)) & 1u;
     if (v == 0 && !nan && p.decay == 1.0f) continue;
-    const float r = (float)fma((double)old[j], (double)p.decay, (double)v * down);
+    const float r = (float)fma((double)old[j], (double)p.decay, (double)v * power(top[i] - s0));
     acc[i] = nan ? __int_as_float(0x7FC00000) : r;
   }
 }
