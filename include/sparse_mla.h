@@ -560,7 +560,13 @@ smla_status sparse_mla_cache_append(const smla_append_shape* shape, const void* 
  * for the entries of the index lists, 0 for entries that are padding (or out
  * of range, which sets bit 2 of the device error word).  lse is the
  * decode's; the weights of a list then sum to 64 (one per head).  A head whose
- * lse is -inf takes no part. */
+ * lse is -inf takes no part.
+ * Scores are accumulated in fp32.  bf16 rows: products of the bf16 values.  Rows
+ * of codes: the codes times the query in two parts of eight bits.  With M the
+ * power of two at or below the head's largest |q|, an element of the query is
+ * exact from 2^-9 M on and within 2^-17 M below for SMLA_KV_FP8_E4M3_ROWSCALE (the
+ * decode's own parts), exact from 2^-13 M on and within 2^-21 M below for the
+ * codes of SMLA_KV_DSV4_PAGED. */
 
 /* Shapes, layouts and checks as for sparse_mla_decode (shape->nsplit is not
  * used); lse [B, 64] fp32 ([B, T, 64]) is read, weights [B, topk] fp32

@@ -69,6 +69,7 @@ struct WtCfg {
 };
 constexpr uint32_t kIdescWt = make_idesc(64, 64, false, false), kIdescWt8 = make_idesc_e4m3(128, 128, false);
 constexpr uint32_t kIdescWtGroup = make_idesc_e4m3(128, 64, false), kIdescWtRope = make_idesc(128, 64, false, false);
+constexpr uint32_t kIdescWtLow = kIdescWtGroup | (1u << 10);         // B e5m2 (format 1 in bits 10-12)
 // barriers
 constexpr int WB_FULL = 0, WB_EMPTY = 4, WB_SF = 8, WB_SE = 10, WB_Q = 12, WB_FIN = 13, WB_ROW = 14, WB_PART = 16;
 
@@ -140,27 +141,34 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, float (&v)[16
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
-// x (f16x2, |x| < 448) = hi + lo in e4m3x2: hi = e4m3(x), lo = e4m3(x - hi)
-__device__ __forceinline__ void split_e4m3x2_f16(uint32_t x, uint32_t& hi, uint32_t& lo) {
+// x (f16x2, |x| < 448) = hi + lo: hi = e4m3(x), lo = e4m3(x - hi), or e5m2(x - hi)
+template <bool kLowE5m2>
+__device__ __forceinline__ void split_f16(uint32_t x, uint32_t& hi, uint32_t& lo) {
   uint16_t h, l;
   uint32_t h16, r16;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(h) : "r"(x));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(h));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r16) : "r"(x), "r"(h16));
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r16));
+  if constexpr (kLowE5m2) asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(l) : "r"(r16));
+  else asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(l) : "r"(r16));
   hi = h;
   lo = l;
 }
 
 // kHeads heads of a row's query (h0 ..) into the B operand, by one warp.
 // bf16 caches: as they are.  Codes: times the power of two that brings the
-// head's largest |q| into [128, 256), split into e4m3 high and low parts
-// (exact for the bf16 values whose parts are e4m3 normals, within 2^-10 of the
-// scaled value otherwise); s_k[h] receives scale over that power.  This runs
-// once per row between two rows' products, at a warp's own pace (a few cycles
-// an instruction), so it is spread over as many warps as there are and kept
-// short: bf16 pairs are scaled as pairs and split as f16 pairs.  (DeepSeek-V4's
-// last 64 dims are scaled alike and stay bf16.)
+// head's largest |q| into [128, 256), split into a high and a low part.  fp8 rows:
+// both e4m3, as in the decode (exact for the bf16 values whose parts are e4m3
+// normals, within 2^-10 of the scaled value otherwise).  DeepSeek-V4: the low part
+// is e5m2, which holds the up to three significant bits that e4m3 leaves of a
+// bf16 value over a range 2^8 times as wide (one dim of a query 300 times the
+// others: errors of the weights 1e-6, with an e4m3 low part 1e-4): exact down to
+// 2^-6 of the scaled value, within 2^-14 below; the decode multiplies these
+// queries as bf16, and its lse comes from there.  s_k[h] receives scale over that
+// power.  This runs once per row between two rows' products, at a warp's own pace
+// (a few cycles an instruction), so it is spread over as many warps as there are
+// and kept short: bf16 pairs are scaled as pairs and split as f16 pairs.
+// (DeepSeek-V4's last 64 dims are scaled alike and stay bf16.)
 template <int kKind, int kHeads>
 __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* smem, uint32_t sbase, int row, int h0,
                                                int lane, float* s_k) {
@@ -214,7 +222,7 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint32_t y = bf16x2_mul(w4[k], up);
-          split_e4m3x2_f16(pack_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)), hi[k], lo[k]);
+          split_f16<C::kDsv4>(pack_f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)), hi[k], lo[k]);
         }
         // eight codes: half of 16-byte chunk (32 u + lane) / 2 of the row
         const int c = (32 * u + lane) >> 1;
@@ -249,8 +257,8 @@ __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* 
 //    columns 0-63 and 64-127 of the buffer.  DeepSeek-V4 codes too, each group
 //    of 64 dims into 64 columns of its own, high and low parts added there
 //    (converting the codes to bf16 instead took 14,400 instructions per 64
-//    entries, 79 us on 128 x 2,048 entries against 40 now, for a relative
-//    error of 1.1e-7 against 1.3e-7, the query's split).
+//    entries, 79 us on 128 x 2,048 entries against 40 so; relative error 1.1e-7
+//    then, 0.7e-7 so).
 //  * Epilogue warps 0-3 take the even tiles, 4-7 the odd ones; a thread has one
 //    entry: of 128-entry tiles all heads, of 64-entry tiles 32, the other 32
 //    being its partner's, sixteen lanes on.  DeepSeek-V4 (one buffer): all eight
@@ -343,8 +351,8 @@ __global__ void __launch_bounds__(WtCfg<kKind>::kThreads, 1) smla_weights_kernel
           const uint64_t dl = dh + (uint64_t)(C::kQPart >> 4);
           mma8_ss_elect(dg, da, dh, kIdescWtGroup, false);
           mma8_ss_elect(dg, da + 2, dh + 2, kIdescWtGroup, true);
-          mma8_ss_elect(dg, da, dl, kIdescWtGroup, true);
-          mma8_ss_elect(dg, da + 2, dl + 2, kIdescWtGroup, true);
+          mma8_ss_elect(dg, da, dl, kIdescWtLow, true);
+          mma8_ss_elect(dg, da + 2, dl + 2, kIdescWtLow, true);
         }
         const uint64_t ra = sw128_desc(a + 448 * kM, 16, 1024), rb = sw128_desc(b + 2 * C::kQPart, 16, 1024);
         mma_set_elect(d + 448u, ra, rb, kIdescWtRope);
