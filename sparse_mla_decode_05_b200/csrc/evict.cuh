@@ -264,11 +264,6 @@ constexpr int kCpBatch = 8;            // rows a thread has in flight
 constexpr int kCpMaxRows = 1024;       // rows per CTA and step
 constexpr int kCpPages = 512;          // pages of a sequence held in shared memory (the rest read as needed)
 
-// a barrier of the cluster's threads that orders no memory
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 template <int kUnit> struct UnitOf;
 template <> struct UnitOf<16> { using T = uint4; };
 template <> struct UnitOf<8> { using T = uint2; };
@@ -281,9 +276,8 @@ template <> struct UnitOf<4> { using T = uint32_t; };
 // rows up to i + R - 1 needed.  A barrier per step, of the CTAs (a cluster) that
 // share the column, puts all of the step's reads before any of its writes, and
 // rows read later lie above them.  (Columns need no order among themselves.)
-// Between CTAs the barrier is a relaxed one: nothing written is read again, and
-// a thread arrives only once the values it loaded are there (it has used
-// them); a releasing barrier waits for the last step's writes too, 4 us a step.
+// Between CTAs it releases and acquires: nothing less orders one CTA's reads
+// before another's writes, although it waits for the last step's writes too.
 // With new pages nothing has to wait.
 //
 // Each step's physical rows are worked out once, by one thread per row and a
@@ -295,7 +289,7 @@ template <> struct UnitOf<4> { using T = uint32_t; };
 // three times as slow.
 template <int kUnit, bool kInPlace>
 __device__ __forceinline__ void compact_column(const CompactParams& p, const EvictPlane& pl, const int* s_from, const int* s_to,
-                                               int2 (*s_rows)[kCpMaxRows], volatile uint32_t* s_used, int column, int n) {
+                                               int2 (*s_rows)[kCpMaxRows], int column, int n) {
   using U = typename UnitOf<kUnit>::T;
   constexpr int kBatch = kUnit == 16 ? kCpBatch : kCpMaxRows / kCpThreads;
   const int b = blockIdx.y, t = threadIdx.x, rank = blockIdx.x % p.ctas;
@@ -339,21 +333,7 @@ __device__ __forceinline__ void compact_column(const CompactParams& p, const Evi
         v[k] = *reinterpret_cast<const U*>(pl.base + (r.x >> 6) * pl.page_stride + (uint32_t)((r.x & 63) * pl.row_stride + col));
     }
     if (base + step < n) prepare(base + step, s_rows[buf ^ 1]);
-    if (kInPlace) {
-      if (p.ctas > 1) {
-        uint32_t used = 0;
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (to[k] >= 0)
-#pragma unroll
-            for (int w = 0; w < kUnit / 4; ++w) used ^= reinterpret_cast<const uint32_t*>(&v[k])[w];
-        s_used[t] = used;
-        __syncwarp();
-        cluster_sync_relaxed();
-      } else {
-        __syncthreads();
-      }
-    }
+    if (kInPlace) evict_sync(p.ctas);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
       if (to[k] >= 0)
@@ -366,7 +346,6 @@ template <bool kInPlace>
 __global__ void __launch_bounds__(kCpThreads, 4) smla_evict_compact_kernel(const __grid_constant__ CompactParams p) {
   __shared__ int s_from[kCpPages], s_to[kCpPages];
   __shared__ int2 s_rows[2][kCpMaxRows];
-  __shared__ uint32_t s_used[kCpThreads];
   grid_dep_wait();
   const int b = blockIdx.y;
   const int n = min(p.new_len[b], p.budget);
@@ -380,9 +359,9 @@ __global__ void __launch_bounds__(kCpThreads, 4) smla_evict_compact_kernel(const
   while (slot < p.plane[k].slot0) --k;
   const EvictPlane& pl = p.plane[k];
   const int column = slot - pl.slot0;
-  if (pl.unit == 16) compact_column<16, kInPlace>(p, pl, s_from, s_to, s_rows, s_used, column, n);
-  else if (pl.unit == 8) compact_column<8, kInPlace>(p, pl, s_from, s_to, s_rows, s_used, column, n);
-  else compact_column<4, kInPlace>(p, pl, s_from, s_to, s_rows, s_used, column, n);
+  if (pl.unit == 16) compact_column<16, kInPlace>(p, pl, s_from, s_to, s_rows, column, n);
+  else if (pl.unit == 8) compact_column<8, kInPlace>(p, pl, s_from, s_to, s_rows, column, n);
+  else compact_column<4, kInPlace>(p, pl, s_from, s_to, s_rows, column, n);
 }
 
 // ------------------------------------------------------------------ host
@@ -475,7 +454,7 @@ static smla_status run_compact(const smla_evict_shape* s, const int32_t* kept, c
   if (k_cache) plane(k_cache, 64 * 256, 256, 16, s->num_key_rows);
   // In place a cluster per column: as many CTAs (a power of two, at most eight)
   // as leave three to an SM (one sequence of 65,536 -> 8,192 bf16 rows: 30 us
-  // with one CTA, 8 with eight).  New pages: a CTA per step.
+  // with one CTA, 9 with eight).  New pages: a CTA per step.
   const int step_rows = (kCpThreads >> log2_lanes) * kCpBatch;
   p.ctas = 1;
   if (in_place) {
