@@ -99,11 +99,10 @@ __global__ void __launch_bounds__(kEvThreads, 1) smla_evict_select_kernel(const 
   float* out = p.acc_out + (size_t)b * p.max_ctx;
   int32_t* kept = p.kept + (size_t)b * p.budget;
   if (n <= p.budget) {
+    evict_sync(ctas);                 // new_len may be ctx_len, which every CTA of the cluster has read by here
     for (int i = rank * kEvThreads + t; i < p.budget; i += ctas * kEvThreads) kept[i] = i < n ? i : -1;
     if (out != acc)
       for (int i = rank * kEvThreads + t; i < n; i += ctas * kEvThreads) out[i] = acc[i];
-    // (new_len may be ctx_len: the value the other CTAs then read clamps to the same n)
-    __syncthreads();
     if (rank == 0 && t == 0) p.new_len[b] = n;
     return;
   }

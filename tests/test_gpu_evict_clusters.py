@@ -55,3 +55,28 @@ def test_rows_of_every_layout(B, n, budget, kind):
         after = planes(kind, kv, rs, keys)
         for k in want:
             assert np.array_equal(after[k], want[k]), (k, turn)
+
+
+@pytest.mark.parametrize("max_ctx", [8192, 8193, 40000, 70000])
+def test_short_contexts_of_long_rows_with_lengths_in_place(max_ctx):
+    """Nothing to evict, one to eight CTAs per sequence, the lengths written where the CTAs read them: out-of-range
+    ones are clamped and reported."""
+    B, budget = 40, max_ctx - 1
+    pps = -(-max_ctx // 64)
+    pt = torch.zeros(B, pps, dtype=torch.int32, device="cuda")
+    kv, _ = random_cache("bf16", 64, 9)
+    before = kv.view(torch.int16).clone()
+    acc = torch.rand(B, max_ctx, device="cuda")
+    lengths = [-5, 0, 1, budget, budget - 1] + [37 * b for b in range(B - 5)]
+    for turn in range(3):
+        ctx = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        out = torch.full_like(acc, 3.0)
+        kept, new_len, _ = api().evict(acc, ctx, budget, page_table=pt, kv=kv, new_len=ctx, acc_out=out)
+        torch.cuda.synchronize()
+        assert new_len is ctx and ctx.tolist() == [max(n, 0) for n in lengths]
+        for b, n in enumerate(lengths):
+            n = max(n, 0)
+            assert torch.equal(kept[b, :n], torch.arange(n, dtype=torch.int32, device="cuda")) and torch.all(kept[b, n:] == -1)
+            assert torch.equal(out[b, :n], acc[b, :n]) and torch.all(out[b, n:] == 3.0)
+        assert api().device_error() == 4
+    assert torch.equal(kv.view(torch.int16), before)
