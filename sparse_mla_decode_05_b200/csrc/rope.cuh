@@ -30,8 +30,9 @@ static_assert(sizeof(smla_rope_shape) == 64 && offsetof(smla_rope_shape, x_token
 // turn is split into the nearest quarter and a rest of at most an eighth
 // either way; sin and cos of the rest (at most pi / 4) are their Taylor
 // series up to x^9 and x^8 (truncation below 2^-28 and 2^-25), turned by the
-// quarter.  Within 2^-23 of the values, in about half the instructions of a
-// general sincos, as the reduction is already done by the integer product.
+// quarter.  Within 2^-22 of the values by the roundings (1.4 x 2^-24 measured), in
+// about half the instructions of a general sincos, as the reduction is already
+// done by the integer product.
 __device__ __forceinline__ void rope_sincos(unsigned long long step, int p, float m, float& c, float& s) {
   const unsigned long long turn = step * (unsigned long long)(long long)p;
   const uint32_t t = (uint32_t)((turn + 0x80000000ull) >> 32);         // 2^-32 turns
@@ -235,7 +236,8 @@ static cudaError_t launch_rope(RopeParams p, const smla_rope_shape* s, bool inte
   const int rot = 2 * p.pairs;
   const int before = in_place ? 0 : s->offset, after = in_place ? 0 : s->dim - s->offset - rot;
   // 16-byte units where every edge they start from is a multiple of 16 bytes
-  // (8,192 x 64 heads x 64 dims: 32 us, element by element 44)
+  // (8,192 x 64 heads x 64 dims of rows 144 bytes apart: 32.5 us, element by
+  // element 44.4)
   auto mult = [&](long long elements) { return elements % kV == 0; };
   const bool vec = (reinterpret_cast<uintptr_t>(p.x) % 16) == 0 && (reinterpret_cast<uintptr_t>(p.y) % 16) == 0 &&
                    mult(p.xt) && mult(p.xh) && mult(p.yt) && mult(p.yh) && mult(s->offset) && mult(after) &&
@@ -249,7 +251,9 @@ static cudaError_t launch_rope(RopeParams p, const smla_rope_shape* s, bool inte
   // with 1 / 4 / 16 heads per thread (64 heads x 64 dims, interleaved, in a
   // graph): 128 tokens 2.2 / 2.1 / 3.9 us, 256 3.2 / 2.2 / 3.9, 1,024 9.0 / 4.1 /
   // 4.0, 2,048 16.1 / 6.4 / 5.5, 16,384 125 / 49 / 44; 16 tokens 1.85 / 2.06 / 3.9.
-  const long long work = s->tokens * s->heads * p.rot_units, fill = 148ll * 2048;
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  const long long work = s->tokens * s->heads * p.rot_units, fill = 2048ll * sms;
   const int per = 3 * work >= 5 * fill ? 16 : (3 * work >= fill ? 4 : 1);
   p.groups = (s->heads + per - 1) / per;
   if (vec)
