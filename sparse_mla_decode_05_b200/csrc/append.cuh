@@ -253,7 +253,8 @@ __global__ void __launch_bounds__(kApWarps * 32, kApCtas) smla_append_kernel(con
       // of them, where that sets the scale: 1 / rms then cancels), within
       // 2^-22, far inside the half step of 2^-4 that the codes round by.  Values as
       // they came have few bits, and can lie on the border between two codes
-      // exactly: their quotient is made exact there by its remainder.
+      // exactly: their quotient is corrected by its remainder, which one fma
+      // gives without rounding (P. Markstein, IBM J. Res. Dev. 34 (1990) 111).
       const float inv = ap_rcp(scale);
       auto exact = [&](float x) -> float {
         const float q = x * inv;
