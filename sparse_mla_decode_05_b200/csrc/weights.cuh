@@ -648,9 +648,8 @@ struct AccumulateParams {
 template <int kRange>
 __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const AccumulateParams p) {
   constexpr int kPos = kRange / kAcThreads;
-  __shared__ long long sum[kRange];         // first the largest |weight| (its bits), then the sum
-  __shared__ uint8_t top[kRange];           // exponent field of the largest |weight|
-  __shared__ uint32_t bad[kRange / 32];     // positions that got a NaN or an infinity
+  __shared__ long long sum[kRange];
+  __shared__ uint32_t top[kRange];          // the largest |weight|, as bits (at most 48 KB in all)
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x, b = blockIdx.y, p0 = blockIdx.x * kRange;
@@ -669,8 +668,10 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
 #pragma unroll
   for (int j = 0; j < kPos; ++j) old[j] = j * kAcThreads + t < here ? acc[j * kAcThreads + t] : 0.f;
 #pragma unroll
-  for (int j = 0; j < kPos; ++j) sum[j * kAcThreads + t] = 0;
-  if (t < kRange / 32) bad[t] = 0;
+  for (int j = 0; j < kPos; ++j) {
+    sum[j * kAcThreads + t] = 0;
+    top[j * kAcThreads + t] = 0;
+  }
   __syncthreads();
   bool any = false, outside = false;
   // place of an entry in the range; -1: it takes no part in the sums
@@ -679,32 +680,21 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
     const uint32_t pos = (uint32_t)entry - (uint32_t)p0, bits = __float_as_uint(fabsf(v));
     if (pos >= (uint32_t)here || bits == 0) return -1;
     any = true;
-    if (bits < 0x7F800000u) {
-      atomicMax(reinterpret_cast<uint32_t*>(&sum[pos]), bits);
-      return (int)pos;
-    }
-    atomicOr(&bad[pos >> 5], 1u << (pos & 31));
-    return -1;
+    atomicMax(&top[pos], bits);                      // (an infinity or a NaN stands above all numbers)
+    return bits < 0x7F800000u ? (int)pos : -1;
   };
 #pragma unroll
   for (int j = 0; j < kAcKeep; ++j) at[j] = look(at[j], wt[j]);
   for (int i = kAcKeep * kAcThreads + t; i < p.entries; i += kAcThreads) look(__ldg(idx + i), __ldg(w + i));
   if (outside && p0 == 0) atomicOr(&g_error_word, 4u);
   if (!__syncthreads_or(any) && p.decay == 1.0f) return;
-#pragma unroll
-  for (int j = 0; j < kPos; ++j) {
-    const int i = j * kAcThreads + t;
-    const uint32_t field = (uint32_t)sum[i] >> 23;
-    top[i] = (uint8_t)(field ? field : 1u);          // (subnormal weights: the smallest normal one's)
-    sum[i] = 0;
-  }
-  __syncthreads();
-  // the largest weight of exponent field f is below 2^(f - 126)
+  // a number of exponent field f is below 2^(f - 126) (subnormal ones: as of field 1)
   const int s0 = 62 - p.log2_entries + 126;
+  auto field = [&](int pos) -> int { return max((int)(top[pos] >> 23), 1); };
   auto power = [](int k) -> double { return __hiloint2double((1023 + k) << 20, 0); };
   auto add = [&](int pos, float v) {
     // 64 bits as two native 32-bit additions with the carry between them
-    const unsigned long long x = (unsigned long long)__double2ll_rn((double)v * power(s0 - top[pos]));
+    const unsigned long long x = (unsigned long long)__double2ll_rn((double)v * power(s0 - field(pos)));
     uint32_t* at2 = reinterpret_cast<uint32_t*>(&sum[pos]);
     const uint32_t before = atomicAdd(at2, (uint32_t)x);
     const uint32_t high = (uint32_t)(x >> 32) + (before + (uint32_t)x < before ? 1u : 0u);
@@ -724,9 +714,9 @@ __global__ void __launch_bounds__(kAcThreads) smla_accumulate_kernel(const Accum
     const int i = j * kAcThreads + t;
     if (i >= here) continue;
     const long long v = sum[i];
-    const bool nan = (bad[i >> 5] >> (i & 31)) & 1u;
+    const bool nan = top[i] >= 0x7F800000u;
     if (v == 0 && !nan && p.decay == 1.0f) continue;
-    const float r = (float)fma((double)old[j], (double)p.decay, (double)v * power(top[i] - s0));
+    const float r = (float)fma((double)old[j], (double)p.decay, (double)v * power(field(i) - s0));
     acc[i] = nan ? __int_as_float(0x7FC00000) : r;
   }
 }
@@ -805,8 +795,8 @@ static smla_status run_accumulate(int batch, int64_t entries, int max_ctx, const
   p.decay = decay;
   void* args[] = {&p};
   // Narrow ranges while each CTA has an SM to itself (every CTA reads the whole
-  // list).  1,024 / 2,048 / 4,096 positions: 16 x 512 entries 2.3 / 2.7 / 3.3 us,
-  // 64 x 4,096 entries 6.2 / 5.1 / 3.9, both over 8,192 positions, in a graph.
+  // list).  1,024 / 2,048 / 4,096 positions: 16 x 512 entries 2.3 / 2.6 / 3.1 us,
+  // 64 x 4,096 entries 6.8 / 4.4 / 3.8, both over 8,192 positions, in a graph.
   const int sms = device_sm_count();
   if (sms <= 0) return SMLA_ERR_CUDA;
   int range = 1024;
