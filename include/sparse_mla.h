@@ -545,9 +545,9 @@ typedef struct {
  * A slot, sequence or page outside its range writes nothing and sets bit 2
  * of the device error word.  Two tokens of one call may not name the same
  * row (it would hold parts of both).  Rows that no token names keep their
- * bytes.  Values are expected finite, and with norm_weight the mean square and
- * 1 / sqrt(mean square + eps) are expected in fp32's range: values up to 2^63,
- * and no row of zeros, or of values below 2^-62 alone, where eps is 0. */
+ * bytes.  Values are expected finite and, with norm_weight, their mean square in
+ * fp32's range: values up to 2^59 and, where eps is 0, one of at least 2^-58 in
+ * the row. */
 smla_status sparse_mla_cache_append(const smla_append_shape* shape, const void* x, const float* norm_weight,
                                     const smla_rope_table* table, const int32_t* positions, const int32_t* slots,
                                     const int32_t* seq, const int32_t* page_table, void* kv_cache,
@@ -581,7 +581,8 @@ smla_status sparse_mla_attn_weights(const smla_shape* shape, const void* q, cons
  *   entries   list entries per sequence, topk (times tokens_per_seq),
  *             1 .. 2^28
  *   max_ctx   width of acc, 1 .. 2^20
- *   indices   [batch, entries] int32 logical positions; negative entries take
+ *   indices   [batch, entries] int32 logical positions (the lists of a paged
+ *             pool; a flat pool's lists name physical rows); negative ones take
  *             no part; one at or past max_ctx takes none and sets bit 2 of
  *             the device error word.  A position may stand in the list many
  *             times.
