@@ -161,14 +161,14 @@ __device__ __forceinline__ void split_f16(uint32_t x, uint32_t& hi, uint32_t& lo
 // both e4m3, as in the decode (exact for the bf16 values whose parts are e4m3
 // normals, within 2^-10 of the scaled value otherwise).  DeepSeek-V4: the low part
 // is e5m2, which holds the up to three significant bits that e4m3 leaves of a
-// bf16 value over a range 2^8 times as wide (one dim of a query 300 times the
-// others: errors of the weights 1e-6, with an e4m3 low part 1e-4): exact down to
-// 2^-6 of the scaled value, within 2^-14 below; the decode multiplies these
-// queries as bf16, and its lse comes from there.  s_k[h] receives scale over that
-// power.  This runs once per row between two rows' products, at a warp's own pace
-// (a few cycles an instruction), so it is spread over as many warps as there are
-// and kept short: bf16 pairs are scaled as pairs and split as f16 pairs.
-// (DeepSeek-V4's last 64 dims are scaled alike and stay bf16.)
+// bf16 value over a range 2^8 times as wide (one dim of 300 beside N(0, 1) ones:
+// largest error of a weight 6e-6 to 1.5e-5 of it, with an e4m3 low part 5e-4 to
+// 1e-3): exact down to 2^-6 of the scaled value, within 2^-14 below; the decode
+// multiplies these queries as bf16, and its lse comes from there.  s_k[h] receives
+// scale over that power.  This runs once per row between two rows' products, at a
+// warp's own pace (a few cycles an instruction), so it is spread over as many
+// warps as there are and kept short: bf16 pairs are scaled as pairs and split as
+// f16 pairs.  (DeepSeek-V4's last 64 dims are scaled alike and stay bf16.)
 template <int kKind, int kHeads>
 __device__ __forceinline__ void wt_stage_query(const WeightsParams& p, uint8_t* smem, uint32_t sbase, int row, int h0,
                                                int lane, float* s_k) {
